@@ -316,6 +316,153 @@ verkv_status verkv_certify_noalloc(int device, void *stream, int32_t units, int3
                                    verkv_head_stats *stats_out, uint32_t *F_out,
                                    uint32_t *err_out);
 
+/* ---------------------------------------------------------------------------------------------
+ * Around the verified context: heads normalised and rotated, and a paged cache for the tokens
+ * that have no place in it -- those decoded since it was compressed, and prompts that a batch
+ * shares.  The paper has no counterpart: these calls surround its decode step.
+ *
+ * All of them take their sizes kv_heads, q_per_kv and head_dim from the context's shape (batch,
+ * layers, n and cap do not matter: a context of n = cap = 1 serves them), run on its stream and
+ * report through its verkv_sync.  They may be captured into a graph.  Unlike the calls above they
+ * restore the caller's current device.  Two-byte types are VERKV_BF16 and VERKV_F16. */
+enum { VERKV_BF16 = 0, VERKV_F16 = 1 };
+
+/* Rows of head_dim consecutive elements: token t's head h starts at element
+ * t * token_stride + h * head_stride of data, which is device memory.  data must be 16-byte
+ * aligned and both strides multiples of 8 elements, >= 0 (a stride of 0 reads one row for
+ * all; an output's rows must not overlap). */
+typedef struct {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} verkv_rows;
+
+/* The position rotation of the first rotary_dim channels of a head (a multiple of 16 up to
+ * head_dim; 0: none).  Channel pair j = 0 .. rotary_dim / 2 - 1 is (j, j + rotary_dim / 2), or
+ * (2 j, 2 j + 1) when interleaved is not 0; at position p it turns by p * inv_freq[j]:
+ * (a, b) -> (a cos - b sin, b cos + a sin).
+ *   turns  device uint64 [rotary_dim / 2], 8-byte aligned: from verkv_rope_turns */
+typedef struct {
+    int32_t rotary_dim;
+    int32_t interleaved;
+    const uint64_t *turns;
+} verkv_rope;
+
+/* turns[j] = frac(inv_freq[j] / (2 pi)) * 2^64, rounded (host arrays of `count` values): the part
+ * of a turn that one position makes, in 64-bit fixed point, so that p * turns[j] mod 2^64 is the
+ * angle of any 32-bit position to within p * 2^-53 of a turn and its reduction to one turn is
+ * exact.  inv_freq must be finite and of magnitude below 2^32 (VERKV_EINVAL). */
+verkv_status verkv_rope_turns(const double *inv_freq, int32_t count, uint64_t *turns);
+
+/* Per-head root-mean-square norm x * w / sqrt(mean(x^2) + eps), before the rotation.  q_weight and
+ * k_weight: device [head_dim] of the rows' type, 16-byte aligned; NULL: those heads are not
+ * normalised.  eps >= 0, finite. */
+typedef struct {
+    const void *q_weight;
+    const void *k_weight;
+    float eps;
+} verkv_head_norm;
+
+/* Norm and rotation of every query and key head in one pass: q_out = rotate(norm(q)) and
+ * k_out = rotate(norm(k)), computed in float32 and rounded once.
+ *   dtype      VERKV_BF16 or VERKV_F16, of every row and weight
+ *   tokens     >= 0 (0: nothing is launched)
+ *   q, q_out   rows of kv_heads * q_per_kv heads; both NULL: no queries
+ *   k, k_out   rows of kv_heads heads; both NULL: no keys
+ *              (an output may be its input itself, with the same strides; other overlap is not
+ *              allowed.  With strides of 2 * head_dim per token and 2 * head_dim * n per head,
+ *              k_out is the key half of kv_full.)
+ *   norm       NULL: no norm
+ *   rope       NULL: no rotation
+ *   positions  device int32 [tokens], may be NULL without a rotation */
+verkv_status verkv_norm_rotate(verkv_ctx *ctx, int32_t dtype, int32_t tokens, const verkv_rows *q,
+                               const verkv_rows *q_out, const verkv_rows *k,
+                               const verkv_rows *k_out, const verkv_head_norm *norm,
+                               const verkv_rope *rope, const int32_t *positions);
+
+/* A pool of pages: [num_pages][kv_heads][page_tokens][2][head_dim], K row then V row of each token
+ * as in kv_full, device, 16-byte aligned.  page_tokens 16, 32, 64, 128 or 256;
+ * num_pages * kv_heads * page_tokens < 2^31. */
+typedef struct {
+    int32_t dtype;
+    int32_t page_tokens;
+    int32_t num_pages;
+    void *kv;
+} verkv_pages;
+
+/* Cached tokens of `rows` sequences (or prefixes): token i of row s is in slot i % page_tokens of
+ * page table[s * stride + i / page_tokens].
+ *   table       device int32 [rows][stride] page ids
+ *   length      device int32 [rows]: how many tokens of each row there are (not read by
+ *               verkv_paged_append); 0 is allowed
+ *   max_length  an upper bound of every length, known on the host, at most
+ *               stride * page_tokens; it sizes the grid, so a graph captured with it serves any
+ *               lengths up to it */
+typedef struct {
+    const int32_t *table;
+    int32_t rows;
+    int32_t stride;
+    const int32_t *length;
+    int32_t max_length;
+} verkv_span;
+
+/* Append tokens to the pages of their sequences: K rows normalised and rotated on the way, V rows
+ * as they are, and, in the same launch, the queries of the same tokens (q, q_out; both NULL: none).
+ *   seq    device int32 [tokens]: row of span->table; -1 marks a padding token, of which no K and V
+ *          are written (its query is still computed)
+ *   index  device int32 [tokens]: the token's place in its sequence (slot of its page as above)
+ *   positions  as in verkv_norm_rotate; it need not equal index
+ * A seq other than -1 outside the table, an index outside 0 .. stride * page_tokens - 1, or a page
+ * id outside the pool is latched (verkv_sync returns VERKV_EINVAL) and that token is skipped.
+ * No two tokens of one call may have the same place.  Nothing else in the pool is written. */
+verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_t tokens,
+                                const verkv_rows *k, const verkv_rows *v, const verkv_rows *q,
+                                const verkv_rows *q_out, const verkv_head_norm *norm,
+                                const verkv_rope *rope, const int32_t *positions,
+                                const int32_t *seq, const int32_t *index, const verkv_span *span);
+
+/* Attention over the paged cache.  Sequence s has the queries q_start[s] .. q_start[s + 1] - 1, its
+ * last tokens: the j-th of c queries sees the first length[s] - c + 1 + j of the sequence's own
+ * cached tokens (append first), all tokens of its group's shared prefix, and what `prior` sums up.
+ *   seqs, q_tokens  >= 0; q_tokens queries in all
+ *   q         rows of kv_heads * q_per_kv heads, of the pages' type
+ *   q_start   device int32 [seqs + 1], ascending from 0 to q_tokens; NULL: one query a sequence
+ *             (q_tokens = seqs)
+ *   own       each sequence's own tokens (rows = seqs), or NULL: none
+ *   prefix    the shared prefixes (rows = groups), or NULL: none.  Each is read once for all the
+ *             queries of its group, however many they are.
+ *   group_start  device int32 [rows of prefix + 1], ascending from 0 to seqs: sequences
+ *             group_start[g] .. group_start[g + 1] - 1 share prefix g; NULL: all share the only one
+ *   scale     of the logits, finite; 0: 1 / sqrt(head_dim)
+ *   prior_o, prior_lse  device float [q_tokens][kv_heads * q_per_kv][head_dim] and
+ *             [q_tokens][kv_heads * q_per_kv]: attention of the same queries over other tokens, as
+ *             verkv_fetch_refine and verkv_attend_dense_host write it, joined to the result; both
+ *             NULL: none.  Where prior_lse is -infinity, prior_o is not used.
+ *   o_out     device [q_tokens][kv_heads * q_per_kv][head_dim] of the pages' type:
+ *             sum exp(l) v / sum exp(l), 0 where a query sees nothing
+ *   lse_out   optional device float [q_tokens][kv_heads * q_per_kv]: log sum exp(l), -infinity
+ *             where a query sees nothing
+ *   workspace device, 256-byte aligned, at least verkv_paged_workspace_size bytes; calls that may
+ *             run at the same time (graphs replayed on other streams among them) need one each
+ * Logits, the running maximum and sum, and the partial sums are float32; the weights are rounded to
+ * the pages' type to be multiplied with V, and not in the sum they are divided by.
+ * What pages hold behind a length is never used, but a value that is not finite inside it reaches
+ * every query of its sequence, also one whose own place comes before it.
+ * A page id outside the pool, a length outside 0 .. max_length, or q_start or group_start not
+ * ascending within their range is latched (verkv_sync returns VERKV_EINVAL); nothing outside the
+ * tensors is read or written, and the outputs of that call are not valid. */
+verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_t seqs,
+                                int32_t q_tokens, const verkv_rows *q, const int32_t *q_start,
+                                const verkv_span *own, const verkv_span *prefix,
+                                const int32_t *group_start, float scale, const float *prior_o,
+                                const float *prior_lse, void *o_out, float *lse_out,
+                                void *workspace, size_t workspace_bytes);
+
+/* Bytes of workspace verkv_paged_attend needs for up to `seqs` sequences, `groups` prefixes (0:
+ * none) and `q_tokens` queries (0 if an argument is out of range). */
+size_t verkv_paged_workspace_size(const verkv_shape *shape, int32_t seqs, int32_t groups,
+                                  int32_t q_tokens);
+
 /* Failure injection, for tests of the error paths (each affects only this context; nothing
  * faults, traps or hangs the GPU):
  *   VERKV_INJECT_COPY_FAIL   value > 0: the next `value` MEMCPY-mode fetch copies fail on the host
@@ -362,6 +509,10 @@ enum {
     VERKV_K_FETCH_GATHER,      /* MEMCPY mode: the host threads' gather of the
                                   fetched rows into page-locked staging (events on
                                   the idle side stream mark its start and end)    */
+    VERKV_K_HEADS,             /* norm and rotation of heads, append to pages     */
+    VERKV_K_PAGED,             /* attention over pages, up to 32 rows a pass      */
+    VERKV_K_PAGED_WIDE,        /* attention over pages, 128 rows and more a pass  */
+    VERKV_K_PAGED_MERGE,       /* joins their partial sums                        */
     VERKV_K_COUNT
 };
 

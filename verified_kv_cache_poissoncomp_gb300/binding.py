@@ -27,6 +27,8 @@ VERKV_SKETCH_Q2 = 1
 VERKV_FETCH_ZEROCOPY = 0
 VERKV_FETCH_MEMCPY = 1
 VERKV_FETCH_KEYS = 4
+VERKV_BF16 = 0
+VERKV_F16 = 1
 
 EXPORTED = ["verkv_sketch_bytes", "verkv_workspace_size", "verkv_create", "verkv_destroy", "verkv_set_fetch_mode",
             "verkv_poissoncomp", "verkv_sketch_build", "verkv_attend_verified",
@@ -35,15 +37,17 @@ EXPORTED = ["verkv_sketch_bytes", "verkv_workspace_size", "verkv_create", "verkv
             "verkv_last_error", "verkv_status_string", "verkv_certify_noalloc",
             "verkv_attend_dense_host", "verkv_set_shortlist", "verkv_shortlist_bitmap",
             "verkv_profile_timeline", "verkv_test_inject", "verkv_measure_sketch_stream",
-            "verkv_set_sequence_offset"]
+            "verkv_set_sequence_offset", "verkv_rope_turns", "verkv_norm_rotate",
+            "verkv_paged_append", "verkv_paged_attend", "verkv_paged_workspace_size"]
 VERKV_INJECT_COPY_FAIL, VERKV_INJECT_BETA_MAXIT, VERKV_INJECT_SCORE_STALL = 1, 2, 3
 VERKV_INJECT_SELECT_GATHER = 4
 # kernel ids (include/verkv.h), in launch order
 (VERKV_K_PC_SOLVE, VERKV_K_PC_GATHER, VERKV_K_SKETCH, VERKV_K_SCORE, VERKV_K_CERTIFY,
  VERKV_K_PARTIAL_PIVOTAL, VERKV_K_FETCH_HOST, VERKV_K_PARTIAL_STAGED, VERKV_K_MERGE,
  VERKV_K_DENSE_HOST, VERKV_K_DENSE_MERGE, VERKV_K_SHORTLIST, VERKV_K_FETCH_COPY,
- VERKV_K_FETCH_GATHER, VERKV_K_COUNT) = range(15)
-# ids that are kernels (the last two time the MEMCPY fetch's copies and host gather)
+ VERKV_K_FETCH_GATHER, VERKV_K_HEADS, VERKV_K_PAGED, VERKV_K_PAGED_WIDE, VERKV_K_PAGED_MERGE,
+ VERKV_K_COUNT) = range(19)
+# ids that are kernels (the two left out time the MEMCPY fetch's copies and host gather)
 KERNEL_IDS = [k for k in range(VERKV_K_COUNT) if k not in (VERKV_K_FETCH_COPY, VERKV_K_FETCH_GATHER)]
 
 
@@ -65,6 +69,31 @@ class verkv_pivotal(ctypes.Structure):
 
 class verkv_sketch(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("data", ctypes.c_void_p)]
+
+
+class verkv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class verkv_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("turns", ctypes.c_void_p)]
+
+
+class verkv_head_norm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class verkv_pages(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("kv", ctypes.c_void_p)]
+
+
+class verkv_span(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("rows", ctypes.c_int32), ("stride", ctypes.c_int32),
+                ("length", ctypes.c_void_p), ("max_length", ctypes.c_int32)]
 
 
 class verkv_head_stats(ctypes.Structure):
@@ -149,6 +178,20 @@ def lib():
         L.verkv_last_error.restype = ctypes.c_char_p
         L.verkv_status_string.argtypes = [ctypes.c_int]
         L.verkv_status_string.restype = ctypes.c_char_p
+        rows, rope, norm = (ctypes.POINTER(t) for t in (verkv_rows, verkv_rope, verkv_head_norm))
+        pages, span = ctypes.POINTER(verkv_pages), ctypes.POINTER(verkv_span)
+        L.verkv_rope_turns.argtypes = [vp, i32, vp]
+        L.verkv_rope_turns.restype = ctypes.c_int
+        L.verkv_norm_rotate.argtypes = [vp, i32, i32, rows, rows, rows, rows, norm, rope, vp]
+        L.verkv_norm_rotate.restype = ctypes.c_int
+        L.verkv_paged_append.argtypes = [vp, pages, i32, rows, rows, rows, rows, norm, rope, vp,
+                                         vp, vp, span]
+        L.verkv_paged_append.restype = ctypes.c_int
+        L.verkv_paged_attend.argtypes = [vp, pages, i32, i32, rows, vp, span, span, vp,
+                                         ctypes.c_float, vp, vp, vp, vp, vp, sz]
+        L.verkv_paged_attend.restype = ctypes.c_int
+        L.verkv_paged_workspace_size.argtypes = [ctypes.POINTER(verkv_shape), i32, i32, i32]
+        L.verkv_paged_workspace_size.restype = sz
         L.verkv_certify_noalloc.argtypes = [ctypes.c_int, vp, i32, i32, i32, i32, vp, vp, vp,
                                             ctypes.c_float, ctypes.c_float, vp, vp, vp]
         L.verkv_certify_noalloc.restype = ctypes.c_int
@@ -303,3 +346,34 @@ def verkv_certify_noalloc(device, stream, units, q_per_kv, head_dim, n, q, sketc
     _check(lib().verkv_certify_noalloc(int(device), stream or None, int(units), int(q_per_kv),
                                        int(head_dim), int(n), q, sketch, r_full, float(eps),
                                        float(delta), stats_out, F_out, err_out))
+
+
+def verkv_rope_turns(inv_freq):
+    """Sequence of floats -> ctypes uint64 array of the same length."""
+    n = len(inv_freq)
+    f, t = (ctypes.c_double * n)(*inv_freq), (ctypes.c_uint64 * n)()
+    _check(lib().verkv_rope_turns(ctypes.cast(f, ctypes.c_void_p), n,
+                                  ctypes.cast(t, ctypes.c_void_p)))
+    return t
+
+
+# In the calls below rows, norm, rope, pages and span are structures of this module, or None.
+def verkv_norm_rotate(ctx, dtype, tokens, q, q_out, k, k_out, norm, rope, positions):
+    _check(lib().verkv_norm_rotate(ctx, dtype, tokens, q, q_out, k, k_out, norm, rope, positions),
+           ctx)
+
+
+def verkv_paged_append(ctx, pages, tokens, k, v, q, q_out, norm, rope, positions, seq, index, span):
+    _check(lib().verkv_paged_append(ctx, pages, tokens, k, v, q, q_out, norm, rope, positions, seq,
+                                    index, span), ctx)
+
+
+def verkv_paged_workspace_size(shape, seqs, groups, q_tokens):
+    return int(lib().verkv_paged_workspace_size(ctypes.byref(shape), seqs, groups, q_tokens))
+
+
+def verkv_paged_attend(ctx, pages, seqs, q_tokens, q, q_start, own, prefix, group_start, scale,
+                       prior_o, prior_lse, o_out, lse_out, workspace, workspace_bytes):
+    _check(lib().verkv_paged_attend(ctx, pages, seqs, q_tokens, q, q_start, own, prefix,
+                                    group_start, scale, prior_o, prior_lse, o_out, lse_out,
+                                    workspace, workspace_bytes), ctx)

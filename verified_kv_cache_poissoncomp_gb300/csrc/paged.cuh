@@ -1,0 +1,304 @@
+// paged.cuh -- argument blocks of the head and paged-attention kernels, and the line of work that
+// the attention kernels share.
+//
+// The line.  Segments are what a set of query rows attends: a shared prefix (rows: every query of
+// its group) or a sequence's own pages (rows: its queries).  A segment splits into units: one KV
+// head and one tile of up to `tt` query tokens, all q_per_kv heads of each.  A unit's work is the
+// number of `tile`-token steps over what its last query sees.  All units' work, laid end to end
+// (segment, head, row tile, step), is cut into equal runs of `per` steps, one for each CTA, wherever
+// the cuts fall: however uneven the lengths are, no CTA has more than one step more than
+// another, a long unit is shared by many CTAs and a CTA takes many short ones.  Lengths are read on
+// the device, so a captured graph follows them.  The piece of unit u in run c goes to the partial
+// slot c + u: walking the line, each step to the next piece raises exactly one of the two.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#include "verkv_common.cuh"
+#endif
+#include "verkv_internal.h"
+
+namespace verkv {
+
+// Norm, rotation and append (k_heads.cu).  Strides in elements; a null weight: that part is not
+// normalised; rd 0: no rotation; pages null: keys go to k_out and there are no values.
+struct HeadsArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *k_out, *pages;
+    long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+    const uint16_t *wq, *wk;
+    const uint64_t *turns;
+    const int32_t *positions, *seq, *index, *table;
+    uint32_t *err;
+    int tokens, hq, hk, hv;  // heads of each token to do: queries, keys, values
+    int chunks;              // warps a token takes (set by the launcher)
+    int rd, interleaved;
+    int table_rows, table_stride, num_pages, page_shift;
+    float eps;
+};
+cudaError_t launch_heads(const HeadsArgs &a, int dtype, int d, cudaStream_t s);
+
+// ---------------------------------------------------------------------------------------------
+struct PagedLevel {
+    const int32_t *table;
+    const int32_t *length;
+    int rows, stride, max_length;  // rows 0: the level is absent
+};
+
+// One launch's share of the work.
+struct PagedLine {
+    int with_prefix, with_own;  // the segments in it: prefixes first
+    int tile;                   // tokens of a step
+    int tt;                     // query tokens of a row tile
+    int ctas;                   // CTAs launched
+    int slots;                  // partial slots there is room for
+    long long *rec;             // {per, 0}, then {work before, units before} of each segment
+    float *part_o;              // [slots][tt * G][d]
+    float *part_ml;             // [slots][tt * G][2]: running maximum (log2 units) and sum
+};
+
+struct PagedArgs {
+    const uint16_t *q;
+    long long q_ts, q_hs;
+    const int32_t *q_start, *group_start;
+    PagedLevel prefix, own;
+    int seqs, q_tokens, hkv, G, page_shift, num_pages;
+    float scale_log2;  // logits are taken in units of log 2
+    uint32_t *err;
+    const float *prior_o, *prior_lse;
+    uint16_t *o;
+    float *lse;
+};
+
+constexpr int PAGED_MAX_CTAS = 512;
+constexpr int PAGED_TILE = 64;        // tokens of a step of k_paged
+constexpr int PAGED_LINES = 2;
+
+cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long long rows, int d, int box_rows);
+cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, int dtype, int d,
+                         cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLine *lines, int dtype, int d, cudaStream_t s);
+
+#ifdef __CUDACC__
+// ---------------------------------------------------------------------------------------------
+struct PagedSeg {
+    int q0, qn, len, row;
+    bool own;
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+__device__ __forceinline__ int paged_segments(const PagedArgs &a, const PagedLine &l) {
+    return (l.with_prefix ? a.prefix.rows : 0) + (l.with_own ? a.own.rows : 0);
+}
+
+// Segment i.  Everything read from the device is clamped to its range, so that no later index
+// leaves the tensors; `bad` is set where that changed something.
+__device__ __forceinline__ PagedSeg paged_segment(const PagedArgs &a, const PagedLine &l, int i, bool &bad) {
+    PagedSeg s;
+    const int np = l.with_prefix ? a.prefix.rows : 0;
+    s.own = i >= np;
+    s.row = s.own ? i - np : i;
+    int s0 = s.row, s1 = s.row + 1;
+    if (!s.own) {
+        const int r0 = a.group_start ? a.group_start[s.row] : 0;
+        const int r1 = a.group_start ? a.group_start[s.row + 1] : a.seqs;
+        s0 = clampi(r0, 0, a.seqs);
+        s1 = clampi(r1, s0, a.seqs);
+        bad |= s0 != r0 || s1 != r1 || (s.row == 0 && r0 != 0) || (s.row == np - 1 && r1 != a.seqs);
+    }
+    const int r0 = a.q_start ? a.q_start[s0] : s0;
+    const int r1 = a.q_start ? a.q_start[s1] : s1;
+    s.q0 = clampi(r0, 0, a.q_tokens);
+    const int q1 = clampi(r1, s.q0, a.q_tokens);
+    bad |= s.q0 != r0 || q1 != r1 || (s0 == 0 && s.q0 != 0) || (s1 == a.seqs && q1 != a.q_tokens);
+    s.qn = q1 - s.q0;
+    const PagedLevel &lv = s.own ? a.own : a.prefix;
+    const int len = lv.length[s.row];
+    s.len = clampi(len, 0, lv.max_length);
+    bad |= s.len != len;
+    return s;
+}
+
+__device__ __forceinline__ int paged_row_tiles(const PagedSeg &s, int tt) { return (s.qn + tt - 1) / tt; }
+
+// Tokens the last query of row tile m sees.
+__device__ __forceinline__ int paged_visible(const PagedSeg &s, int tt, int m) {
+    if (!s.own) return s.len;
+    const int last = min(s.qn, (m + 1) * tt) - 1;
+    return clampi(s.len - (s.qn - 1 - last), 0, s.len);
+}
+__device__ __forceinline__ int paged_steps(const PagedSeg &s, const PagedLine &l, int m) {
+    return (paged_visible(s, l.tt, m) + l.tile - 1) / l.tile;
+}
+// Steps of all row tiles before m, for one head.
+__device__ __forceinline__ long long paged_steps_before(const PagedSeg &s, const PagedLine &l, int m) {
+    if (!s.own) return (long long)m * paged_steps(s, l, 0);
+    long long w = 0;
+    for (int i = 0; i < m; ++i) w += paged_steps(s, l, i);
+    return w;
+}
+
+// Steps of each run, from the whole line's: the same in every CTA.
+__device__ __forceinline__ long long paged_per(long long total, int ctas) {
+    return max(1LL, (total + ctas - 1) / ctas);
+}
+
+// One warp's walk over the run of this CTA.  All lanes hold the same values.
+struct PagedWalk {
+    long long w, w1;   // next step, end of the run
+    long long Wx, Ux;  // work and units before the segment
+    long long per_head;
+    int seg, nt;
+    PagedSeg s;
+    // the current piece
+    int head, m, t0, t1;
+    long long slot;
+
+    __device__ __forceinline__ void load(const PagedArgs &a, const PagedLine &l) {
+        bool bad = false;
+        s = paged_segment(a, l, seg, bad);
+        nt = paged_row_tiles(s, l.tt);
+        per_head = paged_steps_before(s, l, nt);
+    }
+
+    // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also
+    // writes the line's record for the merge and reports bad segments.
+    __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c) {
+        const int lane = threadIdx.x & 31, n = paged_segments(a, l);
+        long long total = 0;
+        bool bad = false;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) {
+            const PagedSeg g = paged_segment(a, l, i, bad);
+            total += paged_steps_before(g, l, paged_row_tiles(g, l.tt)) * a.hkv;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        if (c == 0 && bad) atomicOr(a.err, (uint32_t)ERR_PAGE);
+        const long long per = paged_per(total, l.ctas);
+        w = min(total, (long long)c * per);
+        w1 = min(total, w + per);
+        seg = n;
+        Wx = Ux = 0;
+        if (c != 0 && w >= w1) return;
+        if (c == 0 && lane == 0) l.rec[0] = per;
+        long long wx = 0, ux = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            long long mw = 0, mu = 0;
+            if (i < n) {
+                const PagedSeg g = paged_segment(a, l, i, bad);
+                const int t = paged_row_tiles(g, l.tt);
+                mw = paged_steps_before(g, l, t) * a.hkv;
+                mu = (long long)t * a.hkv;
+            }
+            long long sw = mw, su = mu;  // inclusive sums over the lanes
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long pw = __shfl_up_sync(0xFFFFFFFFu, sw, o), pu = __shfl_up_sync(0xFFFFFFFFu, su, o);
+                if (lane >= o) {
+                    sw += pw;
+                    su += pu;
+                }
+            }
+            const long long ew = wx + sw - mw, eu = ux + su - mu;
+            if (c == 0 && i < n) {
+                l.rec[2 + 2 * i] = ew;
+                l.rec[3 + 2 * i] = eu;
+            }
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, w < w1 && w >= ew && w < ew + mw);
+            if (hit && seg == n) {
+                const int at = __ffs(hit) - 1;
+                seg = i0 + at;
+                Wx = __shfl_sync(0xFFFFFFFFu, ew, at);
+                Ux = __shfl_sync(0xFFFFFFFFu, eu, at);
+                if (c != 0) break;
+            }
+            wx += __shfl_sync(0xFFFFFFFFu, sw, 31);
+            ux += __shfl_sync(0xFFFFFFFFu, su, 31);
+        }
+        if (seg < n) load(a, l); else w = w1;
+    }
+
+    // The next piece; false at the end of the run.
+    __device__ __forceinline__ bool next(const PagedArgs &a, const PagedLine &l, int c) {
+        if (w >= w1) return false;
+        while (w >= Wx + per_head * a.hkv) {
+            if (++seg >= paged_segments(a, l)) return false;
+            Wx += per_head * a.hkv;
+            Ux += (long long)nt * a.hkv;
+            load(a, l);
+        }
+        long long r = w - Wx;
+        head = (int)(r / per_head);
+        r -= head * per_head;
+        m = 0;
+        int steps = paged_steps(s, l, 0);
+        if (!s.own) {
+            m = (int)(r / steps);
+            r -= (long long)m * steps;
+        } else {
+            while (r >= steps) {
+                r -= steps;
+                if (++m >= nt) return false;  // lengths changed under the kernel
+                steps = paged_steps(s, l, m);
+            }
+        }
+        t0 = (int)r;
+        t1 = (int)min((long long)steps, r + (w1 - w));
+        slot = c + Ux + (long long)head * nt + m;
+        w += t1 - t0;
+        return true;
+    }
+};
+
+// 16-bit types of the pages.
+struct PgBf16 {
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t y;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+        return y;
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+struct PgF16 {
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t y;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+        return y;
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+// 2^x to within 2 units of the last place, 0 for -infinity.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+#endif
+
+}  // namespace verkv

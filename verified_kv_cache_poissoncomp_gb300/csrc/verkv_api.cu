@@ -17,6 +17,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "paged.cuh"
 #include "verkv_internal.h"
 
 using namespace verkv;
@@ -323,6 +324,151 @@ cudaError_t copy_rows(verkv_ctx *ctx, void *dst, const void *src, size_t bytes) 
         return cudaErrorInvalidValue;
     }
     return cudaMemcpyAsync(dst, src, bytes, cudaMemcpyHostToDevice, ctx->side);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Heads and the paged cache.
+
+// Puts the caller's current device back when the call returns, on every path.
+class DeviceRestore {
+  public:
+    DeviceRestore() { ok_ = cudaGetDevice(&saved_) == cudaSuccess; }
+    ~DeviceRestore() {
+        if (ok_) cudaSetDevice(saved_);
+    }
+    DeviceRestore(const DeviceRestore &) = delete;
+    DeviceRestore &operator=(const DeviceRestore &) = delete;
+
+  private:
+    int saved_ = 0;
+    bool ok_ = false;
+};
+
+// Rows read or written in 16-byte vectors.
+bool bad_rows(const verkv_rows *r) {
+    return !r->data || bad16(r->data) || r->token_stride < 0 || r->head_stride < 0 || (r->token_stride & 7) ||
+           (r->head_stride & 7);
+}
+// An output of `tokens` x `heads` rows of d elements: no two rows may share an element.
+bool overlapping(const verkv_rows *r, int64_t tokens, int64_t heads, int64_t d) {
+    if (tokens <= 1 && heads <= 1) return false;
+    if (tokens <= 1) return r->head_stride < d;
+    if (heads <= 1) return r->token_stride < d;
+    const bool token_major = r->token_stride >= r->head_stride;
+    const int64_t inner = token_major ? r->head_stride : r->token_stride;
+    const int64_t outer = token_major ? r->token_stride : r->head_stride;
+    const int64_t count = token_major ? heads : tokens;
+    // nested strides, or (a head's rows inside another's stride) interleaved ones such as the key
+    // half of [n][2][d]
+    return inner < d || outer < (count - 1) * inner + d;
+}
+bool valid_dtype(int32_t t) { return t == VERKV_BF16 || t == VERKV_F16; }
+bool valid_pages(const verkv_pages *p, const verkv_shape &sh) {
+    const int t = p->page_tokens;
+    return valid_dtype(p->dtype) && (t == 16 || t == 32 || t == 64 || t == 128 || t == 256) && p->num_pages >= 1 && p->kv &&
+           !bad16(p->kv) && (int64_t)p->num_pages * sh.kv_heads * t < (1LL << 31);
+}
+int page_shift(int page_tokens) {
+    int s = 0;
+    while ((1 << s) < page_tokens) ++s;
+    return s;
+}
+bool valid_rope(const verkv_rope *r, int d) {
+    return r->rotary_dim >= 0 && r->rotary_dim <= d && r->rotary_dim % 16 == 0 &&
+           (r->rotary_dim == 0 || (r->turns && ((uintptr_t)r->turns & 7u) == 0));
+}
+
+// What norm_rotate and append have in common; nullptr, or what is wrong.
+const char *heads_args(const verkv_ctx *ctx, HeadsArgs &a, int32_t dtype, int32_t tokens, const verkv_rows *q,
+                       const verkv_rows *q_out, const verkv_rows *k, const verkv_head_norm *norm,
+                       const verkv_rope *rope, const int32_t *positions) {
+    const int d = ctx->sh.head_dim, hk = ctx->sh.kv_heads, hq = hk * ctx->sh.q_per_kv;
+    if (!valid_dtype(dtype)) return "unknown type";
+    if (tokens < 0) return "tokens must be >= 0";
+    if ((q == nullptr) != (q_out == nullptr)) return "q and q_out come together";
+    if (q) {
+        if (bad_rows(q) || bad_rows(q_out)) return "rows need 16-byte alignment and strides >= 0 that are multiples of 8";
+        if (overlapping(q_out, tokens, hq, d)) return "rows of q_out overlap";
+        a.q = (const uint16_t *)q->data;
+        a.q_ts = q->token_stride;
+        a.q_hs = q->head_stride;
+        a.q_out = (uint16_t *)q_out->data;
+        a.qo_ts = q_out->token_stride;
+        a.qo_hs = q_out->head_stride;
+        a.hq = hq;
+    }
+    if (k) {
+        if (bad_rows(k)) return "rows need 16-byte alignment and strides >= 0 that are multiples of 8";
+        a.k = (const uint16_t *)k->data;
+        a.k_ts = k->token_stride;
+        a.k_hs = k->head_stride;
+        a.hk = hk;
+    }
+    if (norm) {
+        if (!(norm->eps >= 0.0f) || !isfinite(norm->eps)) return "eps must be finite and >= 0";
+        if (bad16(norm->q_weight) || bad16(norm->k_weight)) return "norm weights need 16-byte alignment";
+        a.wq = (const uint16_t *)norm->q_weight;
+        a.wk = (const uint16_t *)norm->k_weight;
+        a.eps = norm->eps;
+    }
+    if (rope) {
+        if (!valid_rope(rope, d)) return "rotary_dim must be a multiple of 16 up to head_dim, turns 8-byte aligned";
+        a.rd = rope->rotary_dim;
+        a.interleaved = rope->interleaved != 0;
+        a.turns = rope->turns;
+        if (a.rd > 0 && !positions) return "a rotation needs positions";
+    }
+    if (bad4(positions)) return "positions need 4-byte alignment";
+    a.positions = positions;
+    a.tokens = tokens;
+    a.err = ctx->err;
+    return nullptr;
+}
+
+constexpr int PAGED_MAX_SEGMENTS = 65536;
+
+// Rows of a segment on average, rounded up, times what a row tile can be.
+int64_t paged_rows(int64_t q_tokens, int64_t segments, int G) { return (q_tokens + segments - 1) / segments * G; }
+
+// Upper bound of the partial rows of any plan for up to these sizes: each level's units cover its
+// queries' rows and at most one ragged row tile a segment, and each CTA adds one slot.
+int64_t paged_rows_bound(int64_t hkv, int64_t G, int64_t seqs, int64_t groups, int64_t q_tokens) {
+    return hkv * (2 * q_tokens * G + 32 * (seqs + groups)) + (int64_t)PAGED_LINES * PAGED_MAX_CTAS * 32;
+}
+bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_shape &sh) {
+    return seqs >= 0 && groups >= 0 && q_tokens >= 0 && seqs <= PAGED_MAX_SEGMENTS && groups <= PAGED_MAX_SEGMENTS &&
+           q_tokens * sh.kv_heads * sh.q_per_kv < (1LL << 31);
+}
+size_t paged_workspace(const verkv_shape &sh, int64_t seqs, int64_t groups, int64_t q_tokens) {
+    const size_t rec = align256((size_t)(2 + 2 * (seqs + groups)) * 8) * PAGED_LINES;
+    const size_t rows = (size_t)paged_rows_bound(sh.kv_heads, sh.q_per_kv, seqs, groups, q_tokens);
+    return rec + rows * (size_t)(sh.head_dim + 2) * 4 + PAGED_LINES * 512;
+}
+
+// Fills in a line over the given segments, taking its buffers from the workspace at `off`.
+void paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows_tile, int ctas_max, unsigned char *ws,
+                size_t &off) {
+    const int64_t hkv = a.hkv;
+    l.tt = rows_tile / a.G;
+    int64_t units = 0, steps = 0, segs = 0;
+    auto level = [&](const PagedLevel &lv) {
+        const int64_t tiles = a.q_tokens / l.tt + lv.rows;
+        units += tiles * hkv;
+        steps += tiles * hkv * ((lv.max_length + l.tile - 1) / l.tile);
+        segs += lv.rows;
+    };
+    if (l.with_prefix) level(a.prefix);
+    if (l.with_own) level(a.own);
+    l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({steps, ctas_max, PAGED_MAX_CTAS}));
+    l.slots = (int)std::min<int64_t>(units + l.ctas, 0x7FFFFFFF);
+    auto take = [&](size_t bytes) {
+        unsigned char *p = ws + off;
+        off = align256(off + bytes);
+        return p;
+    };
+    l.rec = (long long *)take((size_t)(2 + 2 * segs) * 8);
+    l.part_ml = (float *)take((size_t)l.slots * rows_tile * 2 * 4);
+    l.part_o = (float *)take((size_t)l.slots * rows_tile * ctx->sh.head_dim * 4);
 }
 
 }  // namespace
@@ -825,6 +971,8 @@ verkv_status verkv_sync(verkv_ctx *ctx) {
     if (word & ERR_CAPACITY) return fail(ctx, VERKV_ECAPACITY, "pivotal set exceeded cap (truncated)");
     if (word & ERR_TIMEOUT) return fail(ctx, VERKV_ETIMEOUT, "a bounded wait on a copy barrier expired");
     if (word & ERR_BADID) return fail(ctx, VERKV_EINVAL, "a pivotal or fetch row id outside [0, n) (skipped)");
+    if (word & ERR_PAGE)
+        return fail(ctx, VERKV_EINVAL, "a page id, place, length or start outside its range (paged cache)");
     if (word & ERR_BUDGET_SUM) return fail(ctx, VERKV_ENOCONVERGE, "|sum r - eta n| >= 1e-6 n");
     return fail(ctx, VERKV_ENOCONVERGE, "a solve hit its iteration cap");
 }
@@ -888,6 +1036,172 @@ verkv_status verkv_selection_bitmap(verkv_ctx *ctx, uint32_t *out) {
     VERKV_CUDA(cudaMemcpyAsync(out, ctx->F, (size_t)ctx->L.qh_layer * ctx->L.W * 4,
                                cudaMemcpyDefault, ctx->main), "copy F");
     return VERKV_OK;
+}
+
+verkv_status verkv_rope_turns(const double *inv_freq, int32_t count, uint64_t *turns) {
+    if (!inv_freq || !turns || count < 0) return VERKV_EINVAL;
+    for (int32_t i = 0; i < count; ++i)
+        if (!isfinite(inv_freq[i]) || fabs(inv_freq[i]) >= 4294967296.0) return VERKV_EINVAL;
+    for (int32_t i = 0; i < count; ++i) {
+        const double t = inv_freq[i] / 6.283185307179586476925286766559;
+        const double f = t - floor(t);  // [0, 1]: 1 when t is a hair below a whole number
+        const double x = ldexp(f, 64);
+        turns[i] = x >= 18446744073709551616.0 ? 0u : (uint64_t)x;
+    }
+    return VERKV_OK;
+}
+
+verkv_status verkv_norm_rotate(verkv_ctx *ctx, int32_t dtype, int32_t tokens, const verkv_rows *q,
+                               const verkv_rows *q_out, const verkv_rows *k,
+                               const verkv_rows *k_out, const verkv_head_norm *norm,
+                               const verkv_rope *rope, const int32_t *positions) try {
+    if (!ctx) return VERKV_EINVAL;
+    HeadsArgs a{};
+    if (const char *why = heads_args(ctx, a, dtype, tokens, q, q_out, k, norm, rope, positions))
+        return fail(ctx, VERKV_EINVAL, std::string("norm_rotate: ") + why);
+    if ((k == nullptr) != (k_out == nullptr)) return fail(ctx, VERKV_EINVAL, "norm_rotate: k and k_out come together");
+    if (!q && !k) return fail(ctx, VERKV_EINVAL, "norm_rotate: neither queries nor keys");
+    if (k) {
+        if (bad_rows(k_out)) return fail(ctx, VERKV_EINVAL, "norm_rotate: rows need 16-byte alignment and strides >= 0 that are multiples of 8");
+        if (overlapping(k_out, tokens, ctx->sh.kv_heads, ctx->sh.head_dim)) return fail(ctx, VERKV_EINVAL, "norm_rotate: rows of k_out overlap");
+        a.k_out = (uint16_t *)k_out->data;
+        a.ko_ts = k_out->token_stride;
+        a.ko_hs = k_out->head_stride;
+    }
+    if (tokens == 0) return VERKV_OK;
+    const DeviceRestore restore;
+    VERKV_CUDA(cudaSetDevice(ctx->device), "cudaSetDevice");
+    const NvtxRange nvtx("verkv_norm_rotate");
+    VERKV_CUDA(tracked(ctx, VERKV_K_HEADS, ctx->main, [&] { return launch_heads(a, dtype, ctx->sh.head_dim, ctx->main); }), "k_heads");
+    return VERKV_OK;
+} catch (...) {
+    return VERKV_ECUDA;
+}
+
+verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_t tokens,
+                                const verkv_rows *k, const verkv_rows *v, const verkv_rows *q,
+                                const verkv_rows *q_out, const verkv_head_norm *norm,
+                                const verkv_rope *rope, const int32_t *positions,
+                                const int32_t *seq, const int32_t *index, const verkv_span *span) try {
+    if (!ctx) return VERKV_EINVAL;
+    if (!pages || !k || !v || !seq || !index || !span || !span->table) return fail(ctx, VERKV_EINVAL, "paged_append: null pointer");
+    if (!valid_pages(pages, ctx->sh)) return fail(ctx, VERKV_EINVAL, "paged_append: bad pool of pages");
+    if (span->rows < 1 || span->stride < 1) return fail(ctx, VERKV_EINVAL, "paged_append: an empty table");
+    HeadsArgs a{};
+    if (const char *why = heads_args(ctx, a, pages->dtype, tokens, q, q_out, k, norm, rope, positions))
+        return fail(ctx, VERKV_EINVAL, std::string("paged_append: ") + why);
+    if (bad_rows(v)) return fail(ctx, VERKV_EINVAL, "paged_append: rows need 16-byte alignment and strides >= 0 that are multiples of 8");
+    if (bad4(seq) || bad4(index) || bad4(span->table)) return fail(ctx, VERKV_EINVAL, "paged_append: int32 arrays need 4-byte alignment");
+    a.v = (const uint16_t *)v->data;
+    a.v_ts = v->token_stride;
+    a.v_hs = v->head_stride;
+    a.hv = ctx->sh.kv_heads;
+    a.pages = (uint16_t *)pages->kv;
+    a.num_pages = pages->num_pages;
+    a.page_shift = page_shift(pages->page_tokens);
+    a.seq = seq;
+    a.index = index;
+    a.table = span->table;
+    a.table_rows = span->rows;
+    a.table_stride = span->stride;
+    if (tokens == 0) return VERKV_OK;
+    const DeviceRestore restore;
+    VERKV_CUDA(cudaSetDevice(ctx->device), "cudaSetDevice");
+    const NvtxRange nvtx("verkv_paged_append");
+    VERKV_CUDA(tracked(ctx, VERKV_K_HEADS, ctx->main, [&] { return launch_heads(a, pages->dtype, ctx->sh.head_dim, ctx->main); }), "k_heads");
+    return VERKV_OK;
+} catch (...) {
+    return VERKV_ECUDA;
+}
+
+size_t verkv_paged_workspace_size(const verkv_shape *shape, int32_t seqs, int32_t groups, int32_t q_tokens) {
+    if (!valid_shape(shape) || !paged_sizes_ok(seqs, groups, q_tokens, *shape)) return 0;
+    return paged_workspace(*shape, seqs, groups, q_tokens);
+}
+
+verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_t seqs,
+                                int32_t q_tokens, const verkv_rows *q, const int32_t *q_start,
+                                const verkv_span *own, const verkv_span *prefix,
+                                const int32_t *group_start, float scale, const float *prior_o,
+                                const float *prior_lse, void *o_out, float *lse_out,
+                                void *workspace, size_t workspace_bytes) try {
+    if (!ctx) return VERKV_EINVAL;
+    const verkv_shape &sh = ctx->sh;
+    if (!pages || !q || !o_out || !workspace) return fail(ctx, VERKV_EINVAL, "paged_attend: null pointer");
+    if (!valid_pages(pages, sh)) return fail(ctx, VERKV_EINVAL, "paged_attend: bad pool of pages");
+    const int groups = prefix ? prefix->rows : 0;
+    if (!paged_sizes_ok(seqs, groups, q_tokens, sh)) return fail(ctx, VERKV_EINVAL, "paged_attend: too many sequences or queries, or a negative count");
+    if (!q_start && seqs != q_tokens) return fail(ctx, VERKV_EINVAL, "paged_attend: without q_start there is one query a sequence");
+    if (seqs == 0 && q_tokens != 0) return fail(ctx, VERKV_EINVAL, "paged_attend: queries of no sequence");
+    auto bad_span = [&](const verkv_span *s) {
+        return !s->table || !s->length || bad4(s->table) || bad4(s->length) || s->rows < 1 || s->stride < 1 || s->max_length < 0 ||
+               (int64_t)s->max_length > (int64_t)s->stride * pages->page_tokens;
+    };
+    if (seqs > 0 && own && (bad_span(own) || own->rows != seqs)) return fail(ctx, VERKV_EINVAL, "paged_attend: bad table of the sequences' own tokens");
+    if (prefix && bad_span(prefix)) return fail(ctx, VERKV_EINVAL, "paged_attend: bad table of the shared prefixes");
+    if (prefix && !group_start && groups != 1) return fail(ctx, VERKV_EINVAL, "paged_attend: several prefixes need group_start");
+    if (group_start && !prefix) return fail(ctx, VERKV_EINVAL, "paged_attend: group_start without prefixes");
+    if (!isfinite(scale)) return fail(ctx, VERKV_EINVAL, "paged_attend: scale must be finite");
+    if ((prior_o == nullptr) != (prior_lse == nullptr)) return fail(ctx, VERKV_EINVAL, "paged_attend: prior_o and prior_lse come together");
+    if (bad_rows(q)) return fail(ctx, VERKV_EINVAL, "paged_attend: rows need 16-byte alignment and strides >= 0 that are multiples of 8");
+    if (bad16(prior_o) || bad16(o_out) || bad4(prior_lse) || bad4(lse_out) || bad4(q_start) || bad4(group_start))
+        return fail(ctx, VERKV_EINVAL, "paged_attend: prior_o and o_out need 16-byte, other arrays 4-byte alignment");
+    if (((uintptr_t)workspace & 255u) || workspace_bytes < paged_workspace(sh, seqs, groups, q_tokens))
+        return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small or not 256-byte aligned");
+    if (q_tokens == 0) return VERKV_OK;
+    const DeviceRestore restore;
+    VERKV_CUDA(cudaSetDevice(ctx->device), "cudaSetDevice");
+    const NvtxRange nvtx("verkv_paged_attend");
+
+    PagedArgs a{};
+    a.q = (const uint16_t *)q->data;
+    a.q_ts = q->token_stride;
+    a.q_hs = q->head_stride;
+    a.q_start = q_start;
+    a.group_start = group_start;
+    auto level = [](const verkv_span *s) {
+        PagedLevel l{};
+        if (s) l = {s->table, s->length, s->rows, s->stride, s->max_length};
+        return l;
+    };
+    a.prefix = level(prefix && prefix->max_length > 0 ? prefix : nullptr);
+    a.own = level(own && own->max_length > 0 ? own : nullptr);
+    a.seqs = seqs;
+    a.q_tokens = q_tokens;
+    a.hkv = sh.kv_heads;
+    a.G = sh.q_per_kv;
+    a.page_shift = page_shift(pages->page_tokens);
+    a.num_pages = pages->num_pages;
+    a.scale_log2 = (float)((scale == 0.0f ? 1.0 / sqrt((double)sh.head_dim) : (double)scale) * 1.4426950408889634);
+    a.err = ctx->err;
+    a.prior_o = prior_o;
+    a.prior_lse = prior_lse;
+    a.o = (uint16_t *)o_out;
+    a.lse = lse_out;
+
+    PagedLine lines[PAGED_LINES] = {};
+    size_t off = 0;
+    if (a.prefix.rows || a.own.rows) {
+        CUtensorMap map;
+        VERKV_CUDA(paged_tensor_map(&map, pages->kv, pages->dtype, (long long)pages->num_pages * a.hkv * pages->page_tokens,
+                                    sh.head_dim, std::min(pages->page_tokens, PAGED_TILE)), "tensor map of the pages");
+        // One line over both levels.
+        int64_t rows = 0;
+        if (a.prefix.rows) rows = std::max(rows, paged_rows(q_tokens, a.prefix.rows, a.G));
+        if (a.own.rows) rows = std::max(rows, paged_rows(q_tokens, a.own.rows, a.G));
+        PagedLine &l = lines[0];
+        l.with_prefix = a.prefix.rows > 0;
+        l.with_own = a.own.rows > 0;
+        l.tile = PAGED_TILE;
+        const int tile_rows = rows <= 16 ? 16 : 32;
+        paged_line(ctx, a, l, tile_rows, ctx->sms * (tile_rows == 16 ? 2 : 1), (unsigned char *)workspace, off);
+        if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
+        VERKV_CUDA(tracked(ctx, VERKV_K_PAGED, ctx->main, [&] { return launch_paged(a, l, map, pages->dtype, sh.head_dim, ctx->main); }), "k_paged");
+    }
+    VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_MERGE, ctx->main, [&] { return launch_paged_merge(a, lines, pages->dtype, sh.head_dim, ctx->main); }), "k_paged_merge");
+    return VERKV_OK;
+} catch (...) {
+    return VERKV_ECUDA;
 }
 
 verkv_status verkv_test_inject(verkv_ctx *ctx, int what, int64_t value) {
@@ -968,7 +1282,8 @@ const char *verkv_kernel_name(int k) {
     static const char *names[VERKV_K_COUNT] = {
         "k_pc_solve", "k_pc_gather", "k_sketch", "k_score", "k_certify",
         "k_partial(pivotal)", "k_refine", "k_partial(staged)", "k_merge",
-        "k_dense_host", "k_dense_merge", "k_shortlist", "fetch_copy", "fetch_gather"};
+        "k_dense_host", "k_dense_merge", "k_shortlist", "fetch_copy", "fetch_gather",
+        "k_heads", "k_paged", "k_paged_wide", "k_paged_merge"};
     return (k >= 0 && k < VERKV_K_COUNT) ? names[k] : "";
 }
 

@@ -16,6 +16,7 @@ enum : uint32_t {
     ERR_BUDGET_SUM = 1u << 3,  // |sum r - eta n| >= 1e-6 n after the c solve
     ERR_TIMEOUT = 1u << 4,     // a bounded wait on a copy barrier expired
     ERR_BADID = 1u << 5,       // a pivotal or fetch row id outside [0, n) (the row was skipped)
+    ERR_PAGE = 1u << 6,        // a page id, place or length outside its range (see paged.cuh)
 };
 
 // ---------------------------------------------------------------------------------------------

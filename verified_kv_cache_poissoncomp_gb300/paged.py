@@ -1,0 +1,282 @@
+"""Python front end of what surrounds the verified context: per-head norms with the position
+rotation, and a paged cache for tokens that have no place in the compressed context -- those decoded
+since, and prompts that a batch shares.  PyTorch allocates the memory and supplies the stream; the
+work is libverkv's (verkv_norm_rotate, verkv_paged_append, verkv_paged_attend).
+
+    rope = Rope(inv_freq)                                     # float64 frequencies, once
+    cache = PagedKV(kv_heads, q_per_kv, head_dim, num_pages=..., layers=...)
+    q = cache.append(layer, k, v, seq, index, table, positions=pos, rope=rope, q=q, ...)
+    o, lse = cache.attend(layer, q, table, lengths, max_length, prior=(eng.o, eng.lse))
+"""
+import ctypes
+
+import torch
+
+from . import binding as B
+
+_DTYPES = {torch.bfloat16: B.VERKV_BF16, torch.float16: B.VERKV_F16}
+
+
+class Rope:
+    """The rotation of the first 2 * len(inv_freq) channels: pair j turns by position * inv_freq[j]
+    (float64 values; whatever scaling a model gives its frequencies is in them).  interleaved: pairs
+    are neighbours, else rotary_dim / 2 channels apart."""
+
+    def __init__(self, inv_freq, interleaved=False, device=None):
+        f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").reshape(-1).tolist()
+        self.dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        turns = torch.frombuffer(B.verkv_rope_turns(f), dtype=torch.int64) if f else torch.empty(0, dtype=torch.int64)
+        self.turns = turns.to(self.dev)
+        self.desc = B.verkv_rope(2 * len(f), int(bool(interleaved)), self.turns.data_ptr())
+
+
+class PagedKV:
+    """A pool of pages [layers][num_pages][kv_heads][page_tokens][2][head_dim] and the calls on it.
+    Work is issued on the stream that is current when the object is made; a call made while another
+    is current is refused.  One object's calls share its workspace: graphs that may run at the same
+    time need an object each (kv= adopts an existing pool).  With num_pages=0 it has no pool and only
+    norm_rotate."""
+
+    def __init__(self, kv_heads, q_per_kv, head_dim, page_tokens=64, num_pages=0, layers=1,
+                 dtype=torch.bfloat16, device=None, kv=None):
+        self.ctx = None
+        if kv is not None:
+            if kv.dim() != 6 or kv.shape[2] != kv_heads or kv.shape[4] != 2 or kv.shape[5] != head_dim:
+                raise ValueError("kv: [layers][pages][kv_heads][page_tokens][2][head_dim] is required")
+            if not kv.is_cuda or not kv.is_contiguous():
+                raise ValueError("kv: a contiguous CUDA tensor is required")
+            dtype, device = kv.dtype, kv.device
+            layers, num_pages, page_tokens = kv.shape[0], kv.shape[1], kv.shape[3]
+        if dtype not in _DTYPES:
+            raise ValueError("dtype: torch.bfloat16 or torch.float16")
+        self.dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.dev.index is None:
+            self.dev = torch.device("cuda", torch.cuda.current_device())
+        self.dtype, self.h, self.hq, self.d = dtype, kv_heads, kv_heads * q_per_kv, head_dim
+        self.layers = layers
+        self.shape = B.verkv_shape(1, 1, kv_heads, q_per_kv, head_dim, 1, 1)
+        ws = B.verkv_workspace_size(self.shape)
+        if ws == 0:
+            raise B.VerkvError(B.VERKV_EINVAL, "invalid shape")
+        if kv is None and num_pages > 0:
+            kv = torch.zeros((layers, num_pages, kv_heads, page_tokens, 2, head_dim), dtype=dtype, device=self.dev)
+        self.kv = kv
+        self._base = kv.data_ptr() if kv is not None else 0
+        self._layer_bytes = num_pages * kv_heads * page_tokens * 4 * head_dim
+        self._code = _DTYPES[dtype]
+        self._pages = B.verkv_pages(self._code, page_tokens, num_pages, self._base)
+        with torch.cuda.device(self.dev):
+            self.stream = torch.cuda.current_stream(self.dev)
+            self._ctx_ws = torch.empty(ws, dtype=torch.uint8, device=self.dev)
+            self.ctx = B.verkv_create(self.dev.index, self.stream.cuda_stream, self.shape,
+                                      self._ctx_ws.data_ptr(), ws)
+        self._raw_stream = self.stream.cuda_stream
+        # Workspaces of attend, largest last.  None is let go of: a captured graph may hold it.
+        self._spaces, self._needs = [], {}
+
+    # --------------------------------------------------------------------------------------------
+    def _ready(self):
+        if torch.cuda.current_stream(self.dev).cuda_stream != self._raw_stream:
+            raise ValueError("another stream is current than the one this object was made on")
+
+    def _rows(self, t, heads, name):
+        s = t.shape
+        if t.dtype != self.dtype or t.device != self.dev or len(s) != 3 or s[1] != heads or s[2] != self.d:
+            raise ValueError(f"{name}: a {self.dtype} tensor [tokens][{heads}][{self.d}] on {self.dev} is required")
+        st = t.stride()
+        if st[2] != 1 and s[0] > 0:
+            raise ValueError(f"{name}: channels must be contiguous")
+        return B.verkv_rows(t.data_ptr(), st[0] if s[0] > 1 else 0, st[1] if heads > 1 else 0)
+
+    def _ints(self, t, shape, name):
+        if t.dtype != torch.int32 or t.device != self.dev or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous int32 {list(shape)} tensor on {self.dev} is required")
+        return t.data_ptr()
+
+    def _weight(self, t, name):
+        if t is None:
+            return None
+        if t.dtype != self.dtype or t.device != self.dev or tuple(t.shape) != (self.d,) or not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous {self.dtype} [{self.d}] tensor on {self.dev} is required")
+        return t.data_ptr()
+
+    def _rope(self, rope):
+        if rope is None:
+            return None
+        if rope.dev != self.dev:
+            raise ValueError(f"rope: made for {rope.dev}, not {self.dev}")
+        return rope.desc
+
+    def _positions(self, positions, rope, tokens):
+        if positions is None:
+            if rope is not None:
+                raise ValueError("positions: needed for a rotation")
+            return None
+        return self._ints(positions, (tokens,), "positions")
+
+    def _norm(self, q_weight, k_weight, eps):
+        if q_weight is None and k_weight is None:
+            return None
+        return B.verkv_head_norm(self._weight(q_weight, "q_weight"), self._weight(k_weight, "k_weight"), eps)
+
+    def _layer(self, layer):
+        if self.kv is None:
+            raise ValueError("this object has no pages")
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer: 0 .. {self.layers - 1}")
+        self._pages.kv = self._base + layer * self._layer_bytes
+        return self._pages
+
+    # --------------------------------------------------------------------------------------------
+    def norm_rotate(self, q, k, positions=None, rope=None, q_weight=None, k_weight=None, eps=1e-6,
+                    q_out=None, k_out=None):
+        """rotate(norm(q)) and rotate(norm(k)): q [tokens][heads][head_dim] and k
+        [tokens][kv_heads][head_dim], either None, with any token and head strides of whole 16
+        bytes.  An output may be the input itself; by default it is new.  A weight of None leaves
+        those heads as long as they are.  Returns (q_out, k_out)."""
+        self._ready()
+        some = q if q is not None else k
+        if some is None:
+            raise ValueError("q or k is required")
+        tokens = some.shape[0]
+        desc = []
+        outs = []
+        for t, out, heads, name in ((q, q_out, self.hq, "q"), (k, k_out, self.h, "k")):
+            if t is None:
+                if out is not None:
+                    raise ValueError(f"{name}_out: given without {name}")
+                desc += [None, None]
+                outs.append(None)
+                continue
+            if out is None:
+                out = torch.empty((t.shape[0], heads, self.d), dtype=self.dtype, device=self.dev)
+            if t.shape[0] != tokens or out.shape[0] != tokens:
+                raise ValueError(f"{name}: {tokens} tokens are required")
+            desc += [self._rows(t, heads, name), self._rows(out, heads, name + "_out")]
+            outs.append(out)
+        pos = self._positions(positions, rope, tokens)
+        if tokens:
+            B.verkv_norm_rotate(self.ctx, self._code, tokens, *desc, self._norm(q_weight, k_weight, eps),
+                                self._rope(rope), pos)
+        return tuple(outs)
+
+    def append(self, layer, k, v, seq, index, table, positions=None, rope=None, k_weight=None,
+               eps=1e-6, q=None, q_weight=None, q_out=None):
+        """Append tokens to the pages of their sequences: token t of k and v
+        [tokens][kv_heads][head_dim] becomes token index[t] of sequence seq[t] (-1: padding, nothing
+        is written), page table[seq[t]][index[t] // page_tokens]; k is normalised and rotated on the
+        way, and q [tokens][heads][head_dim] in the same launch if it is given.  seq, index and
+        positions: int32 [tokens]; table: int32 [sequences][pages].  Returns q_out (None without q)."""
+        self._ready()
+        tokens = k.shape[0]
+        rk, rv = self._rows(k, self.h, "k"), self._rows(v, self.h, "v")
+        rq = ro = None
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((q.shape[0], self.hq, self.d), dtype=self.dtype, device=self.dev)
+            rq, ro = self._rows(q, self.hq, "q"), self._rows(q_out, self.hq, "q_out")
+            if q.shape[0] != tokens or q_out.shape[0] != tokens:
+                raise ValueError(f"q: {tokens} tokens are required")
+        elif q_out is not None:
+            raise ValueError("q_out: given without q")
+        if v.shape[0] != tokens:
+            raise ValueError(f"v: {tokens} tokens are required")
+        if table.dim() != 2:
+            raise ValueError("table: int32 [sequences][pages] is required")
+        span = B.verkv_span(self._ints(table, tuple(table.shape), "table"), table.shape[0], table.shape[1], None, 0)
+        pos = self._positions(positions, rope, tokens)
+        ps, pi = self._ints(seq, (tokens,), "seq"), self._ints(index, (tokens,), "index")
+        pages = self._layer(layer)
+        if tokens:
+            B.verkv_paged_append(self.ctx, pages, tokens, rk, rv, rq, ro,
+                                 self._norm(q_weight if q is not None else None, k_weight, eps),
+                                 self._rope(rope), pos, ps, pi, span)
+        return q_out
+
+    def attend(self, layer, q, table, lengths, max_length, q_start=None, prefix_table=None,
+               prefix_lengths=None, max_prefix=0, group_start=None, scale=0.0, prior=None, out=None,
+               lse=None):
+        """Attention of q [queries][heads][head_dim] over each sequence's own tokens and, where it
+        is given, the prefix its group shares.
+
+        table, lengths: int32 [sequences][pages] and [sequences] of the own tokens, max_length a
+        bound of the lengths known here (both None: no own tokens).  q_start: int32
+        [sequences + 1], sequence s has the queries q_start[s] .. q_start[s + 1] - 1, which are its
+        last tokens; None: one query each.  prefix_table, prefix_lengths, max_prefix: the same of
+        the shared prefixes; group_start: int32 [prefixes + 1] of sequences, None with one prefix.
+        scale: of the logits, 0 for 1 / sqrt(head_dim).  prior: (o, lse) float32 of attention over
+        other tokens (VerKV.fetch_refine's, say), joined to the result.
+
+        Returns (o [queries][heads][head_dim] of the pool's type, lse float32 [queries][heads])."""
+        self._ready()
+        tokens = q.shape[0]
+        rq = self._rows(q, self.hq, "q")
+        own = prefix = None
+        if table is not None:
+            if table.dim() != 2:
+                raise ValueError("table: int32 [sequences][pages] is required")
+            n = table.shape[0]
+        else:
+            n = tokens if q_start is None else q_start.shape[0] - 1
+        if table is not None and n > 0:
+            own = B.verkv_span(self._ints(table, tuple(table.shape), "table"), n, table.shape[1],
+                               self._ints(lengths, (n,), "lengths"), max_length)
+        ps = self._ints(q_start, (n + 1,), "q_start") if q_start is not None else None
+        groups = 0
+        if prefix_table is not None:
+            if prefix_table.dim() != 2:
+                raise ValueError("prefix_table: int32 [prefixes][pages] is required")
+            groups = prefix_table.shape[0]
+            prefix = B.verkv_span(self._ints(prefix_table, tuple(prefix_table.shape), "prefix_table"), groups,
+                                  prefix_table.shape[1], self._ints(prefix_lengths, (groups,), "prefix_lengths"),
+                                  max_prefix)
+        pg = self._ints(group_start, (groups + 1,), "group_start") if group_start is not None else None
+        po = pl = None
+        if prior is not None:
+            for t, s, name in ((prior[0], tokens * self.hq * self.d, "prior o"), (prior[1], tokens * self.hq, "prior lse")):
+                if t.dtype != torch.float32 or t.device != self.dev or t.numel() != s or not t.is_contiguous():
+                    raise ValueError(f"{name}: a contiguous float32 tensor of {s} values on {self.dev} is required")
+            po, pl = prior[0].data_ptr(), prior[1].data_ptr()
+        if out is None:
+            out = torch.empty((tokens, self.hq, self.d), dtype=self.dtype, device=self.dev)
+        elif out.dtype != self.dtype or out.device != self.dev or tuple(out.shape) != (tokens, self.hq, self.d) or not out.is_contiguous():
+            raise ValueError(f"out: a contiguous {self.dtype} [{tokens}][{self.hq}][{self.d}] tensor on {self.dev} is required")
+        if lse is None:
+            lse = torch.empty((tokens, self.hq), dtype=torch.float32, device=self.dev)
+        elif lse.dtype != torch.float32 or lse.device != self.dev or tuple(lse.shape) != (tokens, self.hq) or not lse.is_contiguous():
+            raise ValueError(f"lse: a contiguous float32 [{tokens}][{self.hq}] tensor on {self.dev} is required")
+        pages = self._layer(layer)
+        if tokens:
+            ws, nbytes = self._space(n, groups, tokens)
+            B.verkv_paged_attend(self.ctx, pages, n, tokens, rq, ps, own, prefix, pg, scale, po, pl,
+                                 out.data_ptr(), lse.data_ptr(), ws, nbytes)
+        return out, lse
+
+    def _space(self, seqs, groups, tokens):
+        need = self._needs.get((seqs, groups, tokens))
+        if need is None:
+            need = self._needs[seqs, groups, tokens] = B.verkv_paged_workspace_size(self.shape, seqs, groups, tokens)
+            if need == 0:
+                raise B.VerkvError(B.VERKV_EINVAL, "too many sequences, prefixes or queries")
+        if not self._spaces or self._spaces[-1].numel() < need:
+            self._spaces.append(torch.empty(need, dtype=torch.uint8, device=self.dev))
+        ws = self._spaces[-1]
+        return ws.data_ptr(), ws.numel()
+
+    def sync(self):
+        """Wait, and raise what the device has reported since the last call."""
+        B.verkv_sync(self.ctx)
+
+    def close(self):
+        if self.ctx is not None:
+            B.verkv_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001 -- interpreter shutdown
+            pass
+
+
+assert ctypes.sizeof(B.verkv_span) == 32
