@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const PagedArgs a, const 
                 if (at >= l.slots) break;
                 const float2 mz = *reinterpret_cast<const float2 *>(l.part_ml + (at * R + in) * 2);
                 float v[V];
-                const float *src = l.part_o + (at * R + in) * D + lane * V;
+                const float *src = l.part_o + at * R * D +
+                                   (l.grouped ? (lane * V / 4) * R * 4 + in * 4 + lane * V % 4 : in * D + lane * V);
                 if (V == 4) {
                     const float4 q = *reinterpret_cast<const float4 *>(src);
                     v[0] = q.x; v[1] = q.y; v[V - 2] = q.z; v[V - 1] = q.w;

@@ -1,0 +1,484 @@
+// k_paged_wide.cu -- attention over the paged cache for many query rows: a prefix that a batch
+// shares, or a sequence with many queries, on the fifth-generation tensor cores.
+//
+// With R rows a KV head, a token costs 4 R d flops and 4 d bytes: from about 280 rows on the
+// products bound it, below that K and V's bytes.  A unit is 128 or 256 rows (query tokens x heads of
+// one KV head); it streams 128-token steps of K and V by TMA into a shared-memory ring, and for
+// every step
+//     S = Q K^T   128 x 128, Q and K in shared memory,       float32 in tensor memory
+//     P = 2^(S c - ref), 16 bits, written over S in tensor memory
+//     O += P V    128 x d, P in tensor memory, V in shared memory
+// Two such chains run side by side so that one's softmax hides behind the other's products: with
+// 256 rows, the two halves of the rows on the same step; with 128 rows, even and odd steps, joined
+// at the unit's end.  Items n = 0, 1, ... alternate between the chains; the products are issued in
+// the order S(0) S(1) | P V(0) S(2) | P V(1) S(3) | ..., in which the tensor core executes them, so
+// that S(n + 2) may overwrite the P that P V(n) reads.
+//
+// Warps: 0-3 and 4-7 hold the rows of the chains, a thread a row (no shuffles); 8 issues the
+// products; 9 walks the line and copies.  The reference `ref` of a row's weights is its running
+// maximum less SHIFT, and is raised -- with O scaled in tensor memory -- only when the maximum has
+// risen by more than SLACK since: rarely after the first steps, and no weight passes
+// 2^(SHIFT + SLACK) <= 2^14.  fp16 weights sit 2^8 up, away from its subnormals.
+#include <float.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "paged.cuh"
+#include "pivotal_mma.cuh"
+#include "tcgen05.cuh"
+#include "verkv_common.cuh"
+
+namespace verkv {
+
+namespace {
+
+constexpr int PW_NT = 320;
+constexpr int PW_MMA = 8, PW_COPY = 9;  // warps
+constexpr int PW_PIECES = 8;            // ring of pieces: the copies are at most a ring of slots ahead
+
+struct PieceDesc {
+    int steps;       // 0: the run is over
+    int tok0;        // first token
+    int vis;         // tokens some row of the unit sees
+    int q0, nq;      // query tokens of the row tile
+    int head;        // KV head
+    int lim0, limd;  // tokens the tile's first query sees, and how many more each next one does
+    int slot;        // partial slot, or -1
+};
+
+template <int D, int TILES>
+struct WideLayout {
+    static constexpr int HALVES = D / 64;
+    static constexpr int BOX = PAGED_WIDE_TILE * 128;   // 128 tokens (or rows) x 64 channels
+    static constexpr int SLOT = HALVES * BOX;           // K or V of a step; also a tile of Q
+    static constexpr int NS = D == 128 ? (TILES == 2 ? 5 : 6) : 10;
+    static constexpr int R = TILES * 128;
+    static constexpr int Q = 0;
+    static constexpr int RING = TILES * SLOT;
+    static constexpr int ML = RING + NS * SLOT;                          // float [2][128][2]
+    static constexpr int PIECES = ML + 2 * 128 * 2 * 4;                  // PieceDesc [PW_PIECES]
+    static constexpr int BARS = (PIECES + PW_PIECES * (int)sizeof(PieceDesc) + 7) / 8 * 8;
+    // full, empty [NS]; piece [PW_PIECES]; s_full, p_full [2]; q_full, o_full, ml_full, drain
+    static constexpr int NBARS = 2 * NS + PW_PIECES + 4 + 4;
+    static constexpr int BYTES = BARS + NBARS * 8 + 16;
+};
+
+template <typename T>
+struct Weights;
+template <>
+struct Weights<PgBf16> {
+    static constexpr float SHIFT = 0.0f, SLACK = 8.0f;
+    static constexpr bool BF = true;
+};
+template <>
+struct Weights<PgF16> {
+    static constexpr float SHIFT = 8.0f, SLACK = 6.0f;
+    static constexpr bool BF = false;
+};
+
+// a * b + c on two floats in one instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float b, float c) {
+    unsigned long long v, bb, cc;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(bb), "l"(cc));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+
+template <typename T, int D, int TILES>
+__global__ void __launch_bounds__(PW_NT, 1)
+    k_paged_wide(const PagedArgs a, const PagedLine l, const int wait_first, const __grid_constant__ CUtensorMap map) {
+    using LY = WideLayout<D, TILES>;
+    using W = Weights<T>;
+    constexpr int NS = LY::NS, R = LY::R;
+    extern __shared__ __align__(1024) unsigned char pw_smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(pw_smem + LY::BARS), *empty = full + NS, *piece = empty + NS;
+    uint64_t *s_full = piece + PW_PIECES, *p_full = s_full + 2, *q_full = p_full + 2, *o_full = q_full + 1;
+    uint64_t *ml_full = o_full + 1, *drain = ml_full + 1;
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_at + 1);
+    PieceDesc *pieces = reinterpret_cast<PieceDesc *>(pw_smem + LY::PIECES);
+    float *ml = reinterpret_cast<float *>(pw_smem + LY::ML);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int k = 0; k < NS; ++k) {
+            mbar_init(&full[k], 1);
+            mbar_init(&empty[k], 1);
+        }
+        for (int k = 0; k < PW_PIECES; ++k) mbar_init(&piece[k], 1);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&s_full[k], 1);
+            mbar_init(&p_full[k], 4);
+        }
+        mbar_init(q_full, 8);
+        mbar_init(o_full, 1);
+        mbar_init(ml_full, 8);
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *abort = 0;
+    }
+    if (warp == PW_MMA) tmem_alloc(tmem_at, 512);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tm = *tmem_at;
+    // S (and P over it) of chain i in columns 128 i .., O in 256 + 128 i ..
+    if (wait_first) pdl_wait();
+    pdl_trigger();
+
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        const bool ok = *abort == 0 && mbar_wait_or_abort(bar, parity & 1u, abort);
+        if (__all_sync(0xFFFFFFFFu, ok)) return true;
+        if (lane == 0) {
+            *abort = 1;
+            raise_error(a.err, ERR_TIMEOUT);
+        }
+        return false;
+    };
+
+    if (warp == PW_COPY) {
+        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+        const int box = min(1 << a.page_shift, PAGED_WIDE_TILE);
+        PagedWalk wk;
+        wk.start(a, l, blockIdx.x);
+        int j = 0, np = 0;  // slots and pieces so far
+        bool go = true;
+        while (go && wk.next(a, l, blockIdx.x)) {
+            const PagedLevel &lv = wk.s.own ? a.own : a.prefix;
+            const int32_t *row = lv.table + (long long)wk.s.row * lv.stride;
+            const int vis = paged_visible(wk.s, l.tt, wk.m);
+            int ids = 0, ids0 = 1, ids1 = 0;  // lane i: id of page ids0 + i of the sequence
+            for (int t = wk.t0; t < wk.t1 && go; ++t) {
+                const int tok0 = t * PAGED_WIDE_TILE, valid = min(PAGED_WIDE_TILE, vis - tok0);
+                const int pages = (valid + box - 1) / box, p0 = tok0 >> a.page_shift;
+                if (p0 < ids0 || p0 + pages > ids1) {
+                    ids0 = p0;
+                    ids1 = p0 + 32;
+                    const int p = p0 + lane;
+                    int id = 0;
+                    if (p <= (vis - 1) >> a.page_shift) {
+                        id = row[p];
+                        if (id < 0 || id >= a.num_pages) {
+                            raise_error(a.err, ERR_PAGE);
+                            id = 0;
+                        }
+                    }
+                    ids = id;
+                }
+                const int id = __shfl_sync(0xFFFFFFFFu, ids, (p0 + lane - ids0) & 31);
+                const int y = (((id * a.hkv + wk.head) << a.page_shift) + ((tok0 + lane * box) & ((1 << a.page_shift) - 1)));
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++j) {
+                    const int k = j % NS;
+                    if (go && j >= NS) go = wait(&empty[k], (uint32_t)(j / NS - 1));
+                    if (!go) break;
+                    if (lane == 0) {
+                        if (kv == 0 && t == wk.t0) {
+                            // A slot was free for this piece's first step, so at most NS / 2 pieces
+                            // are ahead of the products: the entry reused here is long read.
+                            PieceDesc s;
+                            s.steps = wk.t1 - wk.t0;
+                            s.tok0 = tok0;
+                            s.vis = vis;
+                            s.q0 = wk.s.q0 + wk.m * l.tt;
+                            s.nq = min(l.tt, wk.s.qn - wk.m * l.tt);
+                            s.head = wk.head;
+                            s.lim0 = wk.s.own ? wk.s.len - (wk.s.qn - 1 - wk.m * l.tt) : wk.s.len;
+                            s.limd = wk.s.own ? 1 : 0;
+                            s.slot = wk.slot < l.slots ? (int)wk.slot : -1;
+                            if (s.slot < 0) raise_error(a.err, ERR_PAGE);
+                            pieces[np % PW_PIECES] = s;
+                            mbar_arrive(&piece[np % PW_PIECES]);
+                        }
+                        mbar_expect_tx(&full[k], (uint32_t)(pages * box * 2 * D));
+                    }
+                    __syncwarp();
+                    if (lane < pages) {
+                        unsigned char *st = pw_smem + LY::RING + (size_t)k * LY::SLOT + lane * box * 128;
+#pragma unroll
+                        for (int b = 0; b < LY::HALVES; ++b)
+                            tma_load_2d(st + b * LY::BOX, &map, kv * D + b * 64, y, &full[k]);
+                    }
+                    __syncwarp();
+                }
+            }
+            ++np;
+        }
+        if (go && lane == 0) {
+            pieces[np % PW_PIECES].steps = 0;
+            mbar_arrive(&piece[np % PW_PIECES]);
+        }
+        if (!go && lane == 0) {
+            // A wait ran out: let the copies in flight land.  They are the last NS slots issued.
+            for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1));
+        }
+        __syncwarp();
+    } else if (warp == PW_MMA) {
+        const uint32_t ring = smem_addr(pw_smem + LY::RING), qs = smem_addr(pw_smem + LY::Q);
+        constexpr uint32_t IS = mma_desc(128, 128, W::BF, false), IO = mma_desc(128, D, W::BF, true);
+        int j0 = 0;                   // slots before this piece
+        uint32_t ns[2] = {0, 0};      // items of each chain so far
+        for (int np = 0;; ++np) {
+            if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
+            const PieceDesc pd = pieces[np % PW_PIECES];
+            if (pd.steps == 0) break;
+            const int items = pd.steps * TILES;
+            bool go = wait(q_full, (uint32_t)np);
+            tcgen05_after_sync();
+            // S of item n; the slot goes back after its last item.
+            auto do_s = [&](int n) {
+                const int step = n / TILES, tile = n % TILES, i = n & 1, jk = j0 + 2 * step, k = jk % NS;
+                if (tile == 0) go = go && wait(&full[k], (uint32_t)(jk / NS));
+                if (!go) return;
+                if (lane == 0) {
+                    const uint32_t qb = qs + tile * LY::SLOT, kb = ring + k * LY::SLOT;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (ks / 4) * LY::BOX + (ks % 4) * 32;
+                        mma_ss(tm + i * 128, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024), IS, ks > 0);
+                    }
+                    tcgen05_commit(&s_full[i]);
+                    if (tile == TILES - 1) tcgen05_commit(&empty[k]);
+                }
+                __syncwarp();
+            };
+            do_s(0);
+            if (items > 1) do_s(1);
+            for (int n = 0; n < items && go; ++n) {
+                const int step = n / TILES, tile = n % TILES, i = n & 1, jv = j0 + 2 * step + 1, k = jv % NS;
+                const int valid = min(PAGED_WIDE_TILE, pd.vis - (pd.tok0 + step * PAGED_WIDE_TILE));
+                if (tile == 0) {
+                    go = go && wait(&full[k], (uint32_t)(jv / NS));
+                    if (go && (valid & 15)) {
+                        // V rows of the last 16 tokens that nothing sees may hold anything, NaN too: a
+                        // weight of 0 would keep it.
+                        for (int r = valid; r < ((valid + 15) & ~15); ++r)
+                            if (lane < 8 * LY::HALVES)
+                                *reinterpret_cast<uint4 *>(pw_smem + LY::RING + k * LY::SLOT + (lane >> 3) * LY::BOX + r * 128 +
+                                                           (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                go = go && wait(&p_full[i], ns[i]);
+                ++ns[i];
+                if (!go) break;
+                tcgen05_after_sync();
+                if (lane == 0) {
+                    const uint32_t vb = ring + k * LY::SLOT;
+                    const bool first = TILES == 2 ? step == 0 : n < 2;
+                    const int kn = (valid + 15) / 16;
+                    for (int ks = 0; ks < kn; ++ks)
+                        mma_ts(tm + 256 + i * 128, tm + i * 128 + ks * 8, smem_desc(vb + ks * 2048, LY::BOX, 1024), IO,
+                               !first || ks > 0);
+                    if (tile == TILES - 1) tcgen05_commit(&empty[k]);
+                }
+                __syncwarp();
+                if (n + 2 < items) do_s(n + 2);
+            }
+            if (!go) break;
+            if (lane == 0) tcgen05_commit(o_full);
+            __syncwarp();
+            j0 += 2 * pd.steps;
+        }
+        // Nothing of this CTA is in flight when it gives its tensor memory back.
+        if (lane == 0) {
+            tcgen05_commit(drain);
+            if (!mbar_wait_bounded(drain, 0u)) raise_error(a.err, ERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        const int i = warp >> 2;                       // chain
+        const int r = (warp & 3) * 32 + lane;          // row of the tile
+        const int row = TILES == 2 ? i * 128 + r : r;  // row of the unit
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t ts = tm + lanes + i * 128;
+        const float c = fabsf(a.scale_log2);
+        const bool neg = a.scale_log2 < 0.0f;
+        uint32_t ns = 0;
+        for (int np = 0;; ++np) {
+            if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
+            const PieceDesc pd = pieces[np % PW_PIECES];
+            if (pd.steps == 0) break;
+            const int jj = row / a.G, hh = row - jj * a.G;
+            const bool real = jj < pd.nq;
+            const bool busy = __any_sync(0xFFFFFFFFu, real);  // a warp without rows only keeps step
+            // Q, swizzled as the copies are: a thread a row; with one tile the chains halve it.
+            {
+                const uint16_t *src = a.q + (long long)(pd.q0 + (real ? jj : 0)) * a.q_ts + (long long)(pd.head * a.G + hh) * a.q_hs;
+                unsigned char *dst = pw_smem + LY::Q + (TILES == 2 ? i * LY::SLOT : 0);
+                constexpr int N = TILES == 2 ? D / 8 : D / 16;
+                const int c0 = TILES == 2 ? 0 : i * N;
+#pragma unroll
+                for (int x = 0; x < N; ++x) {
+                    const int ch = c0 + x;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (real) v = *reinterpret_cast<const uint4 *>(src + ch * 8);
+                    *reinterpret_cast<uint4 *>(dst + (ch >> 3) * LY::BOX + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            const int lim = real ? pd.lim0 + pd.limd * jj : 0;
+            const int count = TILES == 2 ? pd.steps : (pd.steps + 1 - i) / 2;
+            float ref = -INFINITY, sum = 0.0f;
+            bool ok = true;
+            for (int n = 0; n < count; ++n, ++ns) {
+                if (!(ok = wait(&s_full[i], ns))) break;
+                tcgen05_after_sync();
+                if (busy) {
+                    uint32_t s[128];
+                    tmem_ld128(s, ts);
+                    const int tok0 = pd.tok0 + (TILES == 2 ? n : 2 * n + i) * PAGED_WIDE_TILE;
+                    if (neg) {
+#pragma unroll
+                        for (int x = 0; x < 128; ++x) s[x] ^= 0x80000000u;
+                    }
+                    if (__any_sync(0xFFFFFFFFu, tok0 + PAGED_WIDE_TILE > lim)) {
+#pragma unroll
+                        for (int x = 0; x < 128; ++x) s[x] = tok0 + x < lim ? s[x] : 0xFF800000u;
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) top[x] = __uint_as_float(s[x]);
+#pragma unroll
+                    for (int x = 4; x < 128; ++x) top[x & 3] = fmaxf(top[x & 3], __uint_as_float(s[x]));
+                    const float want = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c - W::SHIFT;
+                    if (__any_sync(0xFFFFFFFFu, want > ref + W::SLACK || (ref == -INFINITY && want != -INFINITY))) {
+                        const float m = fmaxf(ref, want);
+                        const float f = m == ref ? 1.0f : exp2_fast(ref - m);
+                        ref = m;
+                        sum *= f;
+                        if (n > 0) {
+                            // P V(n - 1) of this chain is done: S(n) was issued after it.
+#pragma unroll
+                            for (int x = 0; x < D; x += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(o, tm + lanes + 256 + i * 128 + x);
+#pragma unroll
+                                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                                tmem_st32(tm + lanes + 256 + i * 128 + x, o);
+                            }
+                        }
+                    }
+                    const float base = ref == -INFINITY ? 0.0f : ref;  // a row that sees nothing so far
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            float u = __uint_as_float(s[64 * h + 2 * x]), v = __uint_as_float(s[64 * h + 2 * x + 1]);
+                            fma2(u, v, c, -base);
+                            u = exp2_fast(u);
+                            v = exp2_fast(v);
+                            p[x] = T::pack(u, v);
+                            part[(x & 1) * 2] += u;
+                            part[(x & 1) * 2 + 1] += v;
+                        }
+                        tmem_st32(ts + 32 * h, p);
+                    }
+                    tmem_wait_st();
+                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                }
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[i]);
+            }
+            if (!ok) break;
+            if (TILES == 1) {
+                // Each chain tells the other its rows' reference and sum.
+                ml[(i * 128 + r) * 2] = ref;
+                ml[(i * 128 + r) * 2 + 1] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+                if (!wait(ml_full, (uint32_t)np)) break;
+            }
+            if (!wait(o_full, (uint32_t)np)) break;
+            tcgen05_after_sync();
+            if (busy) {
+                // Partials lie [slot][4-channel group][row]: consecutive rows are written together.
+                float *po = l.part_o + (long long)max(pd.slot, 0) * R * D + row * 4;
+                float *pm = l.part_ml + ((long long)max(pd.slot, 0) * R + row) * 2;
+                const bool put = real && pd.slot >= 0;
+                if (TILES == 2) {
+#pragma unroll
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o, tm + lanes + 256 + i * 128 + x);
+                        if (put) {
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                *reinterpret_cast<uint4 *>(po + (long long)(x / 4 + y) * R * 4) =
+                                    make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                        }
+                    }
+                    if (put) *reinterpret_cast<float2 *>(pm) = make_float2(ref, sum);
+                } else {
+                    const float m0 = ml[r * 2], z0 = ml[r * 2 + 1], m1 = ml[(128 + r) * 2], z1 = ml[(128 + r) * 2 + 1];
+                    const float m = fmaxf(m0, m1), ms = m == -INFINITY ? 0.0f : m;
+                    const float f0 = exp2_fast(m0 - ms), f1 = exp2_fast(m1 - ms);
+                    const bool both = pd.steps > 1;  // else chain 1's columns hold nothing of this unit
+#pragma unroll
+                    for (int x0 = 0; x0 < D / 2; x0 += 32) {
+                        const int x = i * (D / 2) + x0;
+                        uint32_t o[32], o1[32];
+                        tmem_ld32(o, tm + lanes + 256 + x);
+                        if (both) tmem_ld32(o1, tm + lanes + 384 + x);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            float v = __uint_as_float(o[y]) * f0;
+                            if (both) v = fmaf(__uint_as_float(o1[y]), f1, v);
+                            o[y] = __float_as_uint(v);
+                        }
+                        if (put) {
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                *reinterpret_cast<uint4 *>(po + (long long)(x / 4 + y) * R * 4) =
+                                    make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                        }
+                    }
+                    if (put && i == 0) *reinterpret_cast<float2 *>(pm) = make_float2(m, z0 * f0 + z1 * f1);
+                }
+            }
+            tcgen05_before_sync();
+            // The next unit's Q overwrites this one's, and its products these sums: it is announced by
+            // all eight warps (q_full), each after its reads here.
+        }
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp == PW_MMA) tmem_free(tm, 512);
+    if (!wait_first) pdl_wait();  // the launch before this one is done when this one is
+}
+
+}  // namespace
+
+cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype,
+                              int d, cudaStream_t s) {
+    PagedArgs a = args;
+    // a scale that rounds to 0 would make the masked logits' -infinity not a number
+    if (fabsf(a.scale_log2) < FLT_MIN) a.scale_log2 = copysignf(FLT_MIN, a.scale_log2);
+    const int tiles = l.tt * a.G / 128;
+#define VERKV_WIDE(TT, DT, DD, NN)                                                              \
+    if (dtype == DT && d == DD && tiles == NN) {                                                \
+        const size_t smem = WideLayout<DD, NN>::BYTES;                                          \
+        const cudaError_t e = ensure_smem((const void *)k_paged_wide<TT, DD, NN>, smem);        \
+        if (e != cudaSuccess) return e;                                                         \
+        return launch_pdl(k_paged_wide<TT, DD, NN>, dim3(l.ctas), dim3(PW_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
+    }
+    VERKV_WIDE(PgBf16, VERKV_BF16, 128, 1) VERKV_WIDE(PgBf16, VERKV_BF16, 128, 2)
+    VERKV_WIDE(PgBf16, VERKV_BF16, 64, 1) VERKV_WIDE(PgBf16, VERKV_BF16, 64, 2)
+    VERKV_WIDE(PgF16, VERKV_F16, 128, 1) VERKV_WIDE(PgF16, VERKV_F16, 128, 2)
+    VERKV_WIDE(PgF16, VERKV_F16, 64, 1) VERKV_WIDE(PgF16, VERKV_F16, 64, 2)
+#undef VERKV_WIDE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace verkv

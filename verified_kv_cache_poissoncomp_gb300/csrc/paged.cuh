@@ -56,7 +56,8 @@ struct PagedLine {
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
     long long *rec;             // {per, 0}, then {work before, units before} of each segment
-    float *part_o;              // [slots][tt * G][d]
+    int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][d / 4][tt * G][4]
+    float *part_o;
     float *part_ml;             // [slots][tt * G][2]: running maximum (log2 units) and sum
 };
 
@@ -73,13 +74,19 @@ struct PagedArgs {
     float *lse;
 };
 
-constexpr int PAGED_MAX_CTAS = 512;
+constexpr int PAGED_MAX_CTAS = 512;   // of k_paged
+constexpr int PAGED_WIDE_CTAS = 256;  // of k_paged_wide
 constexpr int PAGED_TILE = 64;        // tokens of a step of k_paged
-constexpr int PAGED_LINES = 2;
+constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
+constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
 
 cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long long rows, int d, int box_rows);
 cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, int dtype, int d,
                          cudaStream_t s);
+// wait_first false: the launch before it on the stream is this call's k_paged, which it need not wait
+// for to begin.
+cudaError_t launch_paged_wide(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype,
+                              int d, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLine *lines, int dtype, int d, cudaStream_t s);
 
 #ifdef __CUDACC__

@@ -425,15 +425,23 @@ const char *heads_args(const verkv_ctx *ctx, HeadsArgs &a, int32_t dtype, int32_
     return nullptr;
 }
 
-constexpr int PAGED_MAX_SEGMENTS = 65536;
+constexpr int PAGED_MAX_SEGMENTS = 65536;  // sequences or prefixes of a call
 
-// Rows of a segment on average, rounded up, times what a row tile can be.
+// Rows of a segment, on average and rounded up.
 int64_t paged_rows(int64_t q_tokens, int64_t segments, int G) { return (q_tokens + segments - 1) / segments * G; }
 
-// Upper bound of the partial rows of any plan for up to these sizes: each level's units cover its
-// queries' rows and at most one ragged row tile a segment, and each CTA adds one slot.
+// A level whose segments have more rows than this goes through k_paged_wide, else k_paged.
+constexpr int PAGED_WIDE_ROWS = 32;
+
+// Rows of a row tile.
+int paged_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= PAGED_WIDE_ROWS ? 32 : rows <= 128 ? 128 : 256; }
+
+// Upper bound of the partial rows of any call for up to these sizes.  Of one level: its queries'
+// rows q G, at most one ragged row tile a segment, and one slot a CTA.  A level in tiles of 128 or
+// 256 rows has more than 32 rows a segment on average, so fewer than q G / (33 - G) segments, whose
+// ragged tiles add at most 256 / 25 q G.
 int64_t paged_rows_bound(int64_t hkv, int64_t G, int64_t seqs, int64_t groups, int64_t q_tokens) {
-    return hkv * (2 * q_tokens * G + 32 * (seqs + groups)) + (int64_t)PAGED_LINES * PAGED_MAX_CTAS * 32;
+    return hkv * (2 * 12 * q_tokens * G + 32 * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * 32 + (int64_t)PAGED_WIDE_CTAS * 256;
 }
 bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_shape &sh) {
     return seqs >= 0 && groups >= 0 && q_tokens >= 0 && seqs <= PAGED_MAX_SEGMENTS && groups <= PAGED_MAX_SEGMENTS &&
@@ -459,7 +467,7 @@ void paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     };
     if (l.with_prefix) level(a.prefix);
     if (l.with_own) level(a.own);
-    l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>({steps, ctas_max, PAGED_MAX_CTAS}));
+    l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
     l.slots = (int)std::min<int64_t>(units + l.ctas, 0x7FFFFFFF);
     auto take = [&](size_t bytes) {
         unsigned char *p = ws + off;
@@ -1182,21 +1190,38 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
     PagedLine lines[PAGED_LINES] = {};
     size_t off = 0;
     if (a.prefix.rows || a.own.rows) {
-        CUtensorMap map;
-        VERKV_CUDA(paged_tensor_map(&map, pages->kv, pages->dtype, (long long)pages->num_pages * a.hkv * pages->page_tokens,
-                                    sh.head_dim, std::min(pages->page_tokens, PAGED_TILE)), "tensor map of the pages");
-        // One line over both levels.
-        int64_t rows = 0;
-        if (a.prefix.rows) rows = std::max(rows, paged_rows(q_tokens, a.prefix.rows, a.G));
-        if (a.own.rows) rows = std::max(rows, paged_rows(q_tokens, a.own.rows, a.G));
-        PagedLine &l = lines[0];
-        l.with_prefix = a.prefix.rows > 0;
-        l.with_own = a.own.rows > 0;
-        l.tile = PAGED_TILE;
-        const int tile_rows = rows <= 16 ? 16 : 32;
-        paged_line(ctx, a, l, tile_rows, ctx->sms * (tile_rows == 16 ? 2 : 1), (unsigned char *)workspace, off);
+        // Each level by the rows of its segments; the two lines' launches need not wait for one another.
+        const int64_t rows_prefix = a.prefix.rows ? paged_rows(q_tokens, a.prefix.rows, a.G) : 0;
+        const int64_t rows_own = a.own.rows ? paged_rows(q_tokens, a.own.rows, a.G) : 0;
+        int64_t rows[PAGED_LINES] = {0, 0};
+        for (int w = 0; w < PAGED_LINES; ++w) {
+            lines[w].with_prefix = rows_prefix > 0 && (rows_prefix > PAGED_WIDE_ROWS) == (w == 1);
+            lines[w].with_own = rows_own > 0 && (rows_own > PAGED_WIDE_ROWS) == (w == 1);
+            if (lines[w].with_prefix) rows[w] = rows_prefix;
+            if (lines[w].with_own) rows[w] = std::max(rows[w], rows_own);
+        }
+        lines[0].tile = PAGED_TILE;
+        lines[1].tile = PAGED_WIDE_TILE;
+        lines[1].grouped = 1;
+        const int t0 = paged_tile_rows(rows[0]), t1 = paged_tile_rows(rows[1]);
+        if (rows[0]) paged_line(ctx, a, lines[0], t0, std::min(ctx->sms * (t0 == 16 ? 2 : 1), PAGED_MAX_CTAS), (unsigned char *)workspace, off);
+        if (rows[1]) paged_line(ctx, a, lines[1], t1, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
         if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
-        VERKV_CUDA(tracked(ctx, VERKV_K_PAGED, ctx->main, [&] { return launch_paged(a, l, map, pages->dtype, sh.head_dim, ctx->main); }), "k_paged");
+        CUtensorMap map;
+        auto make_map = [&](int tile) {
+            return paged_tensor_map(&map, pages->kv, pages->dtype, (long long)pages->num_pages * a.hkv * pages->page_tokens,
+                                    sh.head_dim, std::min(pages->page_tokens, tile));
+        };
+        if (rows[0]) {
+            VERKV_CUDA(make_map(PAGED_TILE), "tensor map of the pages");
+            VERKV_CUDA(tracked(ctx, VERKV_K_PAGED, ctx->main, [&] { return launch_paged(a, lines[0], map, pages->dtype, sh.head_dim, ctx->main); }), "k_paged");
+        }
+        if (rows[1]) {
+            VERKV_CUDA(make_map(PAGED_WIDE_TILE), "tensor map of the pages");
+            VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_WIDE, ctx->main, [&] {
+                           return launch_paged_wide(a, lines[1], map, rows[0] == 0 || ctx->prof_on, pages->dtype, sh.head_dim, ctx->main);
+                       }), "k_paged_wide");
+        }
     }
     VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_MERGE, ctx->main, [&] { return launch_paged_merge(a, lines, pages->dtype, sh.head_dim, ctx->main); }), "k_paged_merge");
     return VERKV_OK;
