@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(PG_NT, PagedLayout<D, MT>::CTAS)
                     s.head = wk.head;
                     s.lim0 = wk.s.own ? wk.s.len - (wk.s.qn - 1 - wk.m * l.tt) : wk.s.len;
                     s.limd = wk.s.own ? 1 : 0;
-                    s.slot = wk.slot < l.slots ? (int)wk.slot : -1;
+                    s.slot = wk.slot < l.slots ? wk.slot : -1;
                     if (s.slot < 0) raise_error(a.err, ERR_PAGE);
                     desc[k] = s;
                     mbar_expect_tx(&full[k], (uint32_t)(pages * box * 4 * D));
@@ -452,13 +452,15 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const PagedArgs a, const 
             const int nt = paged_row_tiles(sg, l.tt), mt = j / l.tt;
             const int steps = paged_steps(sg, l, mt);
             if (steps == 0) continue;
-            const long long per = l.rec[0];
-            const long long w0 = l.rec[2 + 2 * i] + head * paged_steps_before(sg, l, nt) + paged_steps_before(sg, l, mt);
-            const long long u = l.rec[3 + 2 * i] + (long long)head * nt + mt;
+            const int per = l.rec[0].x;
+            if (per == 0) continue;  // a bad segment: nothing was done
+            const int2 before = l.rec[1 + i];
+            const int w0 = before.x + head * paged_steps_before(sg, l, nt) + paged_steps_before(sg, l, mt);
+            const int u = before.y + head * nt + mt;
             const int in = (j - mt * l.tt) * a.G + g, R = l.tt * a.G;
-            const long long c0 = w0 / per, c1 = (w0 + steps - 1) / per;
+            const int c0 = w0 / per, c1 = (w0 + steps - 1) / per;
 #pragma unroll 4
-            for (long long c = c0; c <= c1; ++c) {
+            for (int c = c0; c <= c1; ++c) {
                 const long long at = c + u;
                 if (at >= l.slots) break;
                 const float2 mz = *reinterpret_cast<const float2 *>(l.part_ml + (at * R + in) * 2);

@@ -33,8 +33,8 @@ namespace verkv {
 
 namespace {
 
-constexpr int PW_NT = 320;
-constexpr int PW_MMA = 8, PW_COPY = 9;  // warps
+constexpr int PW_NT = 352;
+constexpr int PW_MMA = 8, PW_COPY = 10;  // warps (8 and 9: a chain's products each)
 constexpr int PW_PIECES = 8;            // ring of pieces: the copies are at most a ring of slots ahead
 
 struct PieceDesc {
@@ -59,8 +59,8 @@ struct WideLayout {
     static constexpr int ML = RING + NS * SLOT;                          // float [2][128][2]
     static constexpr int PIECES = ML + 2 * 128 * 2 * 4;                  // PieceDesc [PW_PIECES]
     static constexpr int BARS = (PIECES + PW_PIECES * (int)sizeof(PieceDesc) + 7) / 8 * 8;
-    // full, empty [NS]; piece [PW_PIECES]; s_full, p_full [2]; q_full, o_full, ml_full, drain
-    static constexpr int NBARS = 2 * NS + PW_PIECES + 4 + 4;
+    // full, empty [NS]; piece [PW_PIECES]; s_full, p_full [2]; q_full, o_full, ml_full; drain, turn [2]
+    static constexpr int NBARS = 2 * NS + PW_PIECES + 4 + 7;
     static constexpr int BYTES = BARS + NBARS * 8 + 16;
 };
 
@@ -87,6 +87,15 @@ __device__ __forceinline__ void fma2(float &x, float &y, float b, float c) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
 }
 
+// The pair (x, y) added to the pair v.
+__device__ __forceinline__ void add2(unsigned long long &v, float x, float y) {
+    unsigned long long w;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(x), "f"(y));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+}
+__device__ __forceinline__ float lo2(unsigned long long v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
 template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(PW_NT, 1)
     k_paged_wide(const PagedArgs a, const PagedLine l, const int wait_first, const __grid_constant__ CUtensorMap map) {
@@ -96,8 +105,8 @@ __global__ void __launch_bounds__(PW_NT, 1)
     extern __shared__ __align__(1024) unsigned char pw_smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(pw_smem + LY::BARS), *empty = full + NS, *piece = empty + NS;
     uint64_t *s_full = piece + PW_PIECES, *p_full = s_full + 2, *q_full = p_full + 2, *o_full = q_full + 1;
-    uint64_t *ml_full = o_full + 1, *drain = ml_full + 1;
-    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *ml_full = o_full + 1, *drain = ml_full + 1, *turn = drain + 2;
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(turn + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_at + 1);
     PieceDesc *pieces = reinterpret_cast<PieceDesc *>(pw_smem + LY::PIECES);
     float *ml = reinterpret_cast<float *>(pw_smem + LY::ML);
@@ -106,7 +115,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     if (tid == 0) {
         for (int k = 0; k < NS; ++k) {
             mbar_init(&full[k], 1);
-            mbar_init(&empty[k], 1);
+            mbar_init(&empty[k], TILES);  // the chains that read it
         }
         for (int k = 0; k < PW_PIECES; ++k) mbar_init(&piece[k], 1);
         for (int k = 0; k < 2; ++k) {
@@ -114,9 +123,12 @@ __global__ void __launch_bounds__(PW_NT, 1)
             mbar_init(&p_full[k], 4);
         }
         mbar_init(q_full, 8);
-        mbar_init(o_full, 1);
+        mbar_init(o_full, 2);
         mbar_init(ml_full, 8);
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
+        mbar_init(&turn[0], 1);
+        mbar_init(&turn[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort = 0;
     }
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     pdl_trigger();
 
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = *abort == 0 && mbar_wait_or_abort(bar, parity & 1u, abort);
+        const bool ok = mbar_wait_or_abort(bar, parity & 1u, abort);
         if (__all_sync(0xFFFFFFFFu, ok)) return true;
         if (lane == 0) {
             *abort = 1;
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                             s.head = wk.head;
                             s.lim0 = wk.s.own ? wk.s.len - (wk.s.qn - 1 - wk.m * l.tt) : wk.s.len;
                             s.limd = wk.s.own ? 1 : 0;
-                            s.slot = wk.slot < l.slots ? (int)wk.slot : -1;
+                            s.slot = wk.slot < l.slots ? wk.slot : -1;
                             if (s.slot < 0) raise_error(a.err, ERR_PAGE);
                             pieces[np % PW_PIECES] = s;
                             mbar_arrive(&piece[np % PW_PIECES]);
@@ -216,78 +228,121 @@ __global__ void __launch_bounds__(PW_NT, 1)
             for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1));
         }
         __syncwarp();
-    } else if (warp == PW_MMA) {
-        const uint32_t ring = smem_addr(pw_smem + LY::RING), qs = smem_addr(pw_smem + LY::Q);
-        constexpr uint32_t IS = mma_desc(128, 128, W::BF, false), IO = mma_desc(128, D, W::BF, true);
-        int j0 = 0;                   // slots before this piece
-        uint32_t ns[2] = {0, 0};      // items of each chain so far
-        for (int np = 0;; ++np) {
-            if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
-            const PieceDesc pd = pieces[np % PW_PIECES];
-            if (pd.steps == 0) break;
-            const int items = pd.steps * TILES;
-            bool go = wait(q_full, (uint32_t)np);
-            tcgen05_after_sync();
-            // S of item n; the slot goes back after its last item.
-            auto do_s = [&](int n) {
-                const int step = n / TILES, tile = n % TILES, i = n & 1, jk = j0 + 2 * step, k = jk % NS;
-                if (tile == 0) go = go && wait(&full[k], (uint32_t)(jk / NS));
-                if (!go) return;
-                if (lane == 0) {
-                    const uint32_t qb = qs + tile * LY::SLOT, kb = ring + k * LY::SLOT;
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (ks / 4) * LY::BOX + (ks % 4) * 32;
-                        mma_ss(tm + i * 128, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024), IS, ks > 0);
-                    }
-                    tcgen05_commit(&s_full[i]);
-                    if (tile == TILES - 1) tcgen05_commit(&empty[k]);
-                }
-                __syncwarp();
-            };
-            do_s(0);
-            if (items > 1) do_s(1);
-            for (int n = 0; n < items && go; ++n) {
-                const int step = n / TILES, tile = n % TILES, i = n & 1, jv = j0 + 2 * step + 1, k = jv % NS;
-                const int valid = min(PAGED_WIDE_TILE, pd.vis - (pd.tok0 + step * PAGED_WIDE_TILE));
-                if (tile == 0) {
-                    go = go && wait(&full[k], (uint32_t)(jv / NS));
-                    if (go && (valid & 15)) {
-                        // V rows of the last 16 tokens that nothing sees may hold anything, NaN too: a
-                        // weight of 0 would keep it.
-                        for (int r = valid; r < ((valid + 15) & ~15); ++r)
-                            if (lane < 8 * LY::HALVES)
-                                *reinterpret_cast<uint4 *>(pw_smem + LY::RING + k * LY::SLOT + (lane >> 3) * LY::BOX + r * 128 +
-                                                           (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                }
-                go = go && wait(&p_full[i], ns[i]);
-                ++ns[i];
-                if (!go) break;
-                tcgen05_after_sync();
-                if (lane == 0) {
-                    const uint32_t vb = ring + k * LY::SLOT;
-                    const bool first = TILES == 2 ? step == 0 : n < 2;
-                    const int kn = (valid + 15) / 16;
-                    for (int ks = 0; ks < kn; ++ks)
-                        mma_ts(tm + 256 + i * 128, tm + i * 128 + ks * 8, smem_desc(vb + ks * 2048, LY::BOX, 1024), IO,
-                               !first || ks > 0);
-                    if (tile == TILES - 1) tcgen05_commit(&empty[k]);
-                }
-                __syncwarp();
-                if (n + 2 < items) do_s(n + 2);
-            }
-            if (!go) break;
-            if (lane == 0) tcgen05_commit(o_full);
-            __syncwarp();
-            j0 += 2 * pd.steps;
-        }
-        // Nothing of this CTA is in flight when it gives its tensor memory back.
+    } else if (warp == PW_MMA || warp == PW_MMA + 1) {
+        // One thread a chain: nothing here waits for a warp to reconverge, one chain's waits and
+        // commits hide behind the other's products, and a descriptor is its slot's plus a constant
+        // (its address field counts 16 bytes).
         if (lane == 0) {
-            tcgen05_commit(drain);
-            if (!mbar_wait_bounded(drain, 0u)) raise_error(a.err, ERR_TIMEOUT);
+            const int i = warp - PW_MMA;
+            const uint64_t ring = smem_desc(smem_addr(pw_smem + LY::RING), LY::BOX, 1024);
+            const uint64_t qd = smem_desc(smem_addr(pw_smem + LY::Q + (TILES == 2 ? i * LY::SLOT : 0)), LY::BOX, 1024);
+            constexpr uint32_t IS = mma_desc(128, 128, W::BF, false), IO = mma_desc(128, D, W::BF, true);
+            const uint32_t st = tm + i * 128, ot = tm + 256 + i * 128;
+            auto await = [&](uint64_t *bar, uint32_t parity) -> bool {
+                if (mbar_try_wait(bar, parity & 1u)) return true;
+                if (mbar_wait_or_abort(bar, parity & 1u, abort)) return true;
+                *abort = 1;
+                raise_error(a.err, ERR_TIMEOUT);
+                return false;
+            };
+            // The chains take turns, so that one's softmax falls into the other's products (left to
+            // themselves they fall in step, and both wait together: 4500 cycles a step against 3000).
+            uint32_t turns = 0;
+            auto take = [&]() -> bool { return (i == 0 && turns == 0) || await(&turn[i], turns - (i == 0 ? 1u : 0u)); };
+            auto pass = [&]() {
+                mbar_arrive(&turn[i ^ 1]);
+                ++turns;
+            };
+            int j0 = 0;       // slots used before the piece
+            uint32_t ns = 0;  // items so far
+            bool go = true;
+            for (int np = 0; go; ++np) {
+                if (!await(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
+                const PieceDesc pd = pieces[np % PW_PIECES];
+                if (pd.steps == 0) break;
+                go = await(q_full, (uint32_t)np);
+                tcgen05_after_sync();
+                // This chain's steps: all, or every other one.
+                constexpr int STRIDE = TILES == 2 ? 1 : 2;
+                const int first = TILES == 2 ? 0 : i;
+                int ks = (j0 + 2 * first) % NS, vs = (j0 + 2 * first + 1) % NS;
+                uint32_t kf = (uint32_t)((j0 + 2 * first) / NS), vf = (uint32_t)((j0 + 2 * first + 1) / NS);
+                auto advance = [&](int &k, uint32_t &f) {
+                    k += 2 * STRIDE;
+                    if (k >= NS) {
+                        k -= NS;
+                        ++f;
+                    }
+                };
+                auto do_s = [&]() {
+                    const uint64_t kd = ring + (uint32_t)(ks * (LY::SLOT >> 4));
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const int off = ((x / 4) * LY::BOX + (x % 4) * 32) >> 4;
+                        mma_ss(st, qd + off, kd + off, IS, x > 0);
+                    }
+                };
+                auto done_s = [&]() {
+                    tcgen05_commit(&s_full[i]);
+                    tcgen05_commit(&empty[ks]);
+                    advance(ks, kf);
+                };
+                // Turn 0: the first S.  Turn n + 1: P V of the chain's n-th step, S of its next.  Chain 1
+                // takes an empty turn where it has a step less.
+                const bool any = first < pd.steps;
+                if (any && go) go = await(&full[ks], kf);
+                if (!go || !(go = take())) break;
+                if (any) do_s();
+                pass();
+                if (any) done_s();
+                for (int step = first; step - first < pd.steps && go; step += STRIDE) {
+                    const bool has = step < pd.steps, more = step + STRIDE < pd.steps;
+                    const int valid = min(PAGED_WIDE_TILE, pd.vis - (pd.tok0 + step * PAGED_WIDE_TILE));
+                    if (has) {
+                        if (!(go = await(&full[vs], vf))) break;
+                        if (valid & 15) {
+                            // V rows of the last 16 tokens that nothing sees may hold anything, NaN too: a
+                            // weight of 0 would keep it.  (Both chains may write these zeros.)
+                            unsigned char *v = pw_smem + LY::RING + vs * LY::SLOT;
+#pragma unroll 1
+                            for (int x = valid * 8; x < ((valid + 15) & ~15) * 8; ++x)
+#pragma unroll
+                                for (int h = 0; h < LY::HALVES; ++h)
+                                    *reinterpret_cast<uint4 *>(v + h * LY::BOX + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                        }
+                        if (more && !(go = await(&full[ks], kf))) break;
+                        if (!(go = await(&p_full[i], ns))) break;
+                        ++ns;
+                    }
+                    if (!(go = take())) break;
+                    tcgen05_after_sync();
+                    if (has) {
+                        const uint64_t vd = ring + (uint32_t)(vs * (LY::SLOT >> 4));
+                        const bool add = step != first;
+                        if (valid > PAGED_WIDE_TILE - 16) {
+#pragma unroll
+                            for (int x = 0; x < PAGED_WIDE_TILE / 16; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, add || x > 0);
+                        } else {
+#pragma unroll 1
+                            for (int x = 0; x < (valid + 15) / 16; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, add || x > 0);
+                        }
+                        if (more) do_s();
+                    }
+                    pass();
+                    if (has) {
+                        if (more) done_s();
+                        tcgen05_commit(&empty[vs]);
+                        advance(vs, vf);
+                    }
+                }
+                if (!go) break;
+                tcgen05_commit(o_full);
+                j0 += 2 * pd.steps;
+            }
+            // Nothing of this chain is in flight when the CTA gives its tensor memory back.
+            tcgen05_commit(&drain[i]);
+            if (!mbar_wait_bounded(&drain[i], 0u)) raise_error(a.err, ERR_TIMEOUT);
         }
         __syncwarp();
     } else {
@@ -297,26 +352,37 @@ __global__ void __launch_bounds__(PW_NT, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t ts = tm + lanes + i * 128;
         const float c = fabsf(a.scale_log2);
-        const bool neg = a.scale_log2 < 0.0f;
+        const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // a negative scale turns Q round
         uint32_t ns = 0;
-        for (int np = 0;; ++np) {
-            if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
-            const PieceDesc pd = pieces[np % PW_PIECES];
-            if (pd.steps == 0) break;
-            const int jj = row / a.G, hh = row - jj * a.G;
-            const bool real = jj < pd.nq;
-            const bool busy = __any_sync(0xFFFFFFFFu, real);  // a warp without rows only keeps step
-            // Q, swizzled as the copies are: a thread a row; with one tile the chains halve it.
-            {
+        PieceDesc pd = {};
+        // Round -1 runs the softmax once over whatever tensor memory holds, for its instructions: a
+        // kernel starts with cold instruction caches, and these 10 KB would else be fetched (5 us) when
+        // the first product is ready instead of while its operands are on their way.  No product is
+        // in flight then: the first waits for this warp's Q.
+        for (int np = -1;; ++np) {
+            const bool dry = np < 0;
+            bool real = true, busy = true;
+            int lim = 0, count = 1;
+            if (!dry) {
+                if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
+                pd = pieces[np % PW_PIECES];
+                if (pd.steps == 0) break;
+                const int jj = row / a.G, hh = row - jj * a.G;
+                real = jj < pd.nq;
+                busy = __any_sync(0xFFFFFFFFu, real);  // a warp without rows only keeps step
+                lim = real ? pd.lim0 + pd.limd * jj : 0;
+                count = TILES == 2 ? pd.steps : (pd.steps + 1 - i) / 2;
+                // Q, swizzled as the copies are: a thread a row; with one tile the chains halve it.
                 const uint16_t *src = a.q + (long long)(pd.q0 + (real ? jj : 0)) * a.q_ts + (long long)(pd.head * a.G + hh) * a.q_hs;
                 unsigned char *dst = pw_smem + LY::Q + (TILES == 2 ? i * LY::SLOT : 0);
                 constexpr int N = TILES == 2 ? D / 8 : D / 16;
                 const int c0 = TILES == 2 ? 0 : i * N;
-#pragma unroll
+#pragma unroll 4
                 for (int x = 0; x < N; ++x) {
                     const int ch = c0 + x;
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
                     if (real) v = *reinterpret_cast<const uint4 *>(src + ch * 8);
+                    v = make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
                     *reinterpret_cast<uint4 *>(dst + (ch >> 3) * LY::BOX + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
                 }
                 fence_proxy_async_smem();
@@ -324,21 +390,16 @@ __global__ void __launch_bounds__(PW_NT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
             }
-            const int lim = real ? pd.lim0 + pd.limd * jj : 0;
-            const int count = TILES == 2 ? pd.steps : (pd.steps + 1 - i) / 2;
             float ref = -INFINITY, sum = 0.0f;
             bool ok = true;
-            for (int n = 0; n < count; ++n, ++ns) {
-                if (!(ok = wait(&s_full[i], ns))) break;
+#pragma unroll 1
+            for (int n = 0; n < count; ++n) {
+                if (!dry && !(ok = wait(&s_full[i], ns))) break;
                 tcgen05_after_sync();
                 if (busy) {
                     uint32_t s[128];
                     tmem_ld128(s, ts);
                     const int tok0 = pd.tok0 + (TILES == 2 ? n : 2 * n + i) * PAGED_WIDE_TILE;
-                    if (neg) {
-#pragma unroll
-                        for (int x = 0; x < 128; ++x) s[x] ^= 0x80000000u;
-                    }
                     if (__any_sync(0xFFFFFFFFu, tok0 + PAGED_WIDE_TILE > lim)) {
 #pragma unroll
                         for (int x = 0; x < 128; ++x) s[x] = tok0 + x < lim ? s[x] : 0xFF800000u;
@@ -356,7 +417,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                         sum *= f;
                         if (n > 0) {
                             // P V(n - 1) of this chain is done: S(n) was issued after it.
-#pragma unroll
+#pragma unroll 1
                             for (int x = 0; x < D; x += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(o, tm + lanes + 256 + i * 128 + x);
@@ -367,7 +428,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                         }
                     }
                     const float base = ref == -INFINITY ? 0.0f : ref;  // a row that sees nothing so far
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    unsigned long long part[2] = {0ull, 0ull};  // pairs of floats
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t p[32];
@@ -378,18 +439,20 @@ __global__ void __launch_bounds__(PW_NT, 1)
                             u = exp2_fast(u);
                             v = exp2_fast(v);
                             p[x] = T::pack(u, v);
-                            part[(x & 1) * 2] += u;
-                            part[(x & 1) * 2 + 1] += v;
+                            add2(part[x & 1], u, v);
                         }
                         tmem_st32(ts + 32 * h, p);
                     }
                     tmem_wait_st();
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    sum += (lo2(part[0]) + hi2(part[0])) + (lo2(part[1]) + hi2(part[1]));
                 }
+                if (dry) break;
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[i]);
+                ++ns;
             }
+            if (dry) continue;
             if (!ok) break;
             if (TILES == 1) {
                 // Each chain tells the other its rows' reference and sum.
@@ -407,7 +470,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                 float *pm = l.part_ml + ((long long)max(pd.slot, 0) * R + row) * 2;
                 const bool put = real && pd.slot >= 0;
                 if (TILES == 2) {
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < D; x += 32) {
                         uint32_t o[32];
                         tmem_ld32(o, tm + lanes + 256 + i * 128 + x);
@@ -424,7 +487,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                     const float m = fmaxf(m0, m1), ms = m == -INFINITY ? 0.0f : m;
                     const float f0 = exp2_fast(m0 - ms), f1 = exp2_fast(m1 - ms);
                     const bool both = pd.steps > 1;  // else chain 1's columns hold nothing of this unit
-#pragma unroll
+#pragma unroll 1
                     for (int x0 = 0; x0 < D / 2; x0 += 32) {
                         const int x = i * (D / 2) + x0;
                         uint32_t o[32], o1[32];

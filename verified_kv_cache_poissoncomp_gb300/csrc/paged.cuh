@@ -6,8 +6,7 @@
 // head and one tile of up to `tt` query tokens, all q_per_kv heads of each.  A unit's work is the
 // number of `tile`-token steps over what its last query sees.  All units' work, laid end to end
 // (segment, head, row tile, step), is cut into equal runs of `per` steps, one for each CTA, wherever
-// the cuts fall: however uneven the lengths are, no CTA has more than one step more than
-// another, a long unit is shared by many CTAs and a CTA takes many short ones.  Lengths are read on
+// the cuts fall: however uneven the lengths are, no CTA has more than `per` steps, a long unit is shared by many CTAs and a CTA takes many short ones.  Lengths are read on
 // the device, so a captured graph follows them.  The piece of unit u in run c goes to the partial
 // slot c + u: walking the line, each step to the next piece raises exactly one of the two.
 #pragma once
@@ -55,7 +54,7 @@ struct PagedLine {
     int tt;                     // query tokens of a row tile
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
-    long long *rec;             // {per, 0}, then {work before, units before} of each segment
+    int2 *rec;                  // {per, 0}, then {work before, units before} of each segment; per 0: no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][d / 4][tt * G][4]
     float *part_o;
     float *part_ml;             // [slots][tt * G][2]: running maximum (log2 units) and sum
@@ -142,28 +141,23 @@ __device__ __forceinline__ int paged_steps(const PagedSeg &s, const PagedLine &l
     return (paged_visible(s, l.tt, m) + l.tile - 1) / l.tile;
 }
 // Steps of all row tiles before m, for one head.
-__device__ __forceinline__ long long paged_steps_before(const PagedSeg &s, const PagedLine &l, int m) {
-    if (!s.own) return (long long)m * paged_steps(s, l, 0);
-    long long w = 0;
+__device__ __forceinline__ int paged_steps_before(const PagedSeg &s, const PagedLine &l, int m) {
+    if (!s.own) return m * paged_steps(s, l, 0);
+    int w = 0;
     for (int i = 0; i < m; ++i) w += paged_steps(s, l, i);
     return w;
 }
 
-// Steps of each run, from the whole line's: the same in every CTA.
-__device__ __forceinline__ long long paged_per(long long total, int ctas) {
-    return max(1LL, (total + ctas - 1) / ctas);
-}
-
-// One warp's walk over the run of this CTA.  All lanes hold the same values.
+// One warp's walk over the run of this CTA.  All lanes hold the same values.  The host has checked
+// that a whole line's steps and units fit 31 bits; a segment outside its range empties the line.
 struct PagedWalk {
-    long long w, w1;   // next step, end of the run
-    long long Wx, Ux;  // work and units before the segment
-    long long per_head;
-    int seg, nt;
+    int w, w1;   // next step, end of the run
+    int Wx, Ux;  // work and units before the segment
+    int per_head;
+    int seg, n, nt;
     PagedSeg s;
     // the current piece
-    int head, m, t0, t1;
-    long long slot;
+    int head, m, t0, t1, slot;
 
     __device__ __forceinline__ void load(const PagedArgs &a, const PagedLine &l) {
         bool bad = false;
@@ -175,48 +169,52 @@ struct PagedWalk {
     // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also
     // writes the line's record for the merge and reports bad segments.
     __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c) {
-        const int lane = threadIdx.x & 31, n = paged_segments(a, l);
-        long long total = 0;
+        const int lane = threadIdx.x & 31;
+        n = paged_segments(a, l);
+        int total = 0;
         bool bad = false;
-#pragma unroll 4
+#pragma unroll 1
         for (int i = lane; i < n; i += 32) {
             const PagedSeg g = paged_segment(a, l, i, bad);
             total += paged_steps_before(g, l, paged_row_tiles(g, l.tt)) * a.hkv;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-        if (c == 0 && bad) atomicOr(a.err, (uint32_t)ERR_PAGE);
-        const long long per = paged_per(total, l.ctas);
-        w = min(total, (long long)c * per);
+        total = __reduce_add_sync(0xFFFFFFFFu, total);
+        bad = __any_sync(0xFFFFFFFFu, bad);
+        if (bad) total = 0;
+        const int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
+        w = min((long long)total, (long long)c * per);
         w1 = min(total, w + per);
         seg = n;
-        Wx = Ux = 0;
-        if (c != 0 && w >= w1) return;
-        if (c == 0 && lane == 0) l.rec[0] = per;
-        long long wx = 0, ux = 0;
+        if (c == 0 && lane == 0) {
+            l.rec[0] = make_int2(per, 0);
+            if (bad) raise_error(a.err, ERR_PAGE);
+        }
+        if (bad || (c != 0 && w >= w1)) {
+            w = w1;
+            return;
+        }
+        int wx = 0, ux = 0;
+#pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += 32) {
             const int i = i0 + lane;
-            long long mw = 0, mu = 0;
+            int mw = 0, mu = 0;
             if (i < n) {
                 const PagedSeg g = paged_segment(a, l, i, bad);
                 const int t = paged_row_tiles(g, l.tt);
                 mw = paged_steps_before(g, l, t) * a.hkv;
-                mu = (long long)t * a.hkv;
+                mu = t * a.hkv;
             }
-            long long sw = mw, su = mu;  // inclusive sums over the lanes
+            int sw = mw, su = mu;  // inclusive sums over the lanes
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long pw = __shfl_up_sync(0xFFFFFFFFu, sw, o), pu = __shfl_up_sync(0xFFFFFFFFu, su, o);
+                const int pw = __shfl_up_sync(0xFFFFFFFFu, sw, o), pu = __shfl_up_sync(0xFFFFFFFFu, su, o);
                 if (lane >= o) {
                     sw += pw;
                     su += pu;
                 }
             }
-            const long long ew = wx + sw - mw, eu = ux + su - mu;
-            if (c == 0 && i < n) {
-                l.rec[2 + 2 * i] = ew;
-                l.rec[3 + 2 * i] = eu;
-            }
+            const int ew = wx + sw - mw, eu = ux + su - mu;
+            if (c == 0 && i < n) l.rec[1 + i] = make_int2(ew, eu);
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, w < w1 && w >= ew && w < ew + mw);
             if (hit && seg == n) {
                 const int at = __ffs(hit) - 1;
@@ -235,19 +233,19 @@ struct PagedWalk {
     __device__ __forceinline__ bool next(const PagedArgs &a, const PagedLine &l, int c) {
         if (w >= w1) return false;
         while (w >= Wx + per_head * a.hkv) {
-            if (++seg >= paged_segments(a, l)) return false;
+            if (++seg >= n) return false;  // lengths changed under the kernel
             Wx += per_head * a.hkv;
-            Ux += (long long)nt * a.hkv;
+            Ux += nt * a.hkv;
             load(a, l);
         }
-        long long r = w - Wx;
-        head = (int)(r / per_head);
+        int r = w - Wx;
+        head = (unsigned)r / (unsigned)per_head;
         r -= head * per_head;
         m = 0;
         int steps = paged_steps(s, l, 0);
         if (!s.own) {
-            m = (int)(r / steps);
-            r -= (long long)m * steps;
+            m = (unsigned)r / (unsigned)steps;
+            r -= m * steps;
         } else {
             while (r >= steps) {
                 r -= steps;
@@ -255,9 +253,9 @@ struct PagedWalk {
                 steps = paged_steps(s, l, m);
             }
         }
-        t0 = (int)r;
-        t1 = (int)min((long long)steps, r + (w1 - w));
-        slot = c + Ux + (long long)head * nt + m;
+        t0 = r;
+        t1 = min(steps, r + (w1 - w));
+        slot = c + Ux + head * nt + m;
         w += t1 - t0;
         return true;
     }

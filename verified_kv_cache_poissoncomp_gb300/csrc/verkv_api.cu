@@ -448,13 +448,14 @@ bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_
            q_tokens * sh.kv_heads * sh.q_per_kv < (1LL << 31);
 }
 size_t paged_workspace(const verkv_shape &sh, int64_t seqs, int64_t groups, int64_t q_tokens) {
-    const size_t rec = align256((size_t)(2 + 2 * (seqs + groups)) * 8) * PAGED_LINES;
+    const size_t rec = align256((size_t)(1 + seqs + groups) * 8) * PAGED_LINES;
     const size_t rows = (size_t)paged_rows_bound(sh.kv_heads, sh.q_per_kv, seqs, groups, q_tokens);
     return rec + rows * (size_t)(sh.head_dim + 2) * 4 + PAGED_LINES * 512;
 }
 
-// Fills in a line over the given segments, taking its buffers from the workspace at `off`.
-void paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows_tile, int ctas_max, unsigned char *ws,
+// Fills in a line over the given segments, taking its buffers from the workspace at `off`; false if
+// its work cannot be counted in 31 bits.
+bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows_tile, int ctas_max, unsigned char *ws,
                 size_t &off) {
     const int64_t hkv = a.hkv;
     l.tt = rows_tile / a.G;
@@ -468,15 +469,17 @@ void paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     if (l.with_prefix) level(a.prefix);
     if (l.with_own) level(a.own);
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
-    l.slots = (int)std::min<int64_t>(units + l.ctas, 0x7FFFFFFF);
+    if (steps >= (1LL << 31) || units + l.ctas >= (1LL << 31)) return false;
+    l.slots = (int)(units + l.ctas);
     auto take = [&](size_t bytes) {
         unsigned char *p = ws + off;
         off = align256(off + bytes);
         return p;
     };
-    l.rec = (long long *)take((size_t)(2 + 2 * segs) * 8);
+    l.rec = (int2 *)take((size_t)(1 + segs) * 8);
     l.part_ml = (float *)take((size_t)l.slots * rows_tile * 2 * 4);
     l.part_o = (float *)take((size_t)l.slots * rows_tile * ctx->sh.head_dim * 4);
+    return true;
 }
 
 }  // namespace
@@ -1204,8 +1207,10 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         lines[1].tile = PAGED_WIDE_TILE;
         lines[1].grouped = 1;
         const int t0 = paged_tile_rows(rows[0]), t1 = paged_tile_rows(rows[1]);
-        if (rows[0]) paged_line(ctx, a, lines[0], t0, std::min(ctx->sms * (t0 == 16 ? 2 : 1), PAGED_MAX_CTAS), (unsigned char *)workspace, off);
-        if (rows[1]) paged_line(ctx, a, lines[1], t1, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
+        bool ok = true;
+        if (rows[0]) ok &= paged_line(ctx, a, lines[0], t0, std::min(ctx->sms * (t0 == 16 ? 2 : 1), PAGED_MAX_CTAS), (unsigned char *)workspace, off);
+        if (rows[1]) ok &= paged_line(ctx, a, lines[1], t1, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
+        if (!ok) return fail(ctx, VERKV_EINVAL, "paged_attend: more than 2^31 steps of work in one call");
         if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
         CUtensorMap map;
         auto make_map = [&](int tile) {
