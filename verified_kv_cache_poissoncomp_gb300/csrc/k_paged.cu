@@ -2,16 +2,17 @@
 //
 //   o = sum_i 2^(l_i - m) v_i / sum_i 2^(l_i - m),   l_i = q . k_i scale log2(e), m the running maximum
 //
-// k_paged: up to 32 query rows (query tokens x heads of one KV head) against a run of cached tokens.
+// k_paged: up to 16 query rows (query tokens x heads of one KV head) against a run of cached tokens.
 // Bound by the bytes of K and V: a decode step has q_per_kv rows a sequence, a few flops per byte.
 // One warp walks the CTA's run of the line (paged.cuh) and copies 64-token steps of K and V into
-// a shared-memory ring by TMA (boxes of one page's tokens x 64 channels, 128-byte swizzle); what a
-// step is (which rows, which tokens, whether a unit begins or ends with it) travels beside it, so
-// one thread's walk drives the CTA.  Four warps take 16 tokens of a step each: S = Q K^T with the
-// rows as the m16 of mma.m16n8k16 (K by ldmatrix), the softmax in registers -- each warp keeps its
-// own running maximum and sum and rescales only when some row's maximum rises -- and P, already
-// in the A operand's layout, times V (ldmatrix, transposed).  At a unit's end the four warps' states
-// are joined in shared memory and written as one partial.
+// a shared-memory ring by TMA (boxes of one page's tokens x 64 channels, 128-byte swizzle), with a
+// unit's queries beside its first step; what a step is (which rows, which tokens, whether a unit
+// begins or ends with it) travels with it, so one warp's walk drives the CTA and runs ahead of it.
+// Four warps take 16 tokens of a step each: S = Q K^T with the rows as the m16 of mma.m16n8k16 (K by
+// ldmatrix), the softmax in registers -- each warp keeps its own running maximum and sum and rescales
+// only when some row's maximum rises -- and P, already in the A operand's layout, times V (ldmatrix,
+// transposed).  At a unit's end the four warps' states are joined in the step's own shared memory,
+// which nothing reads any more, and written as one partial.
 //
 // k_paged_merge: a warp per query token and head joins the partials of its prefix and its own
 // pages, and the caller's prior state, in a fixed order.
@@ -29,44 +30,64 @@ namespace {
 
 constexpr int PG_CONS = 4;                     // consumer warps: 16 tokens of a step each
 constexpr int PG_NT = 32 * (PG_CONS + 1);      // and one warp that walks and copies
+constexpr int PG_R = PAGED_ROWS;               // rows of a unit: the m16 of an mma
+constexpr int PG_CTAS = 2;                     // an SM
 
 struct StepDesc {
     int flags;       // PG_FIRST | PG_LAST | PG_END
     int valid;       // tokens of the step that some row of the unit sees
     int tok0;        // the step's first token
-    int q0, nq;      // query tokens of the row tile
-    int head;        // KV head
+    int rows;        // real rows
     int lim0, limd;  // tokens the tile's first query sees, and how many more each next one does
     int slot;        // partial slot, or -1
 };
 enum { PG_FIRST = 1, PG_LAST = 2, PG_END = 4 };
 
-template <int D, int MT>
+template <int D>
 struct PagedLayout {
     static constexpr int HALVES = D / 64;
     static constexpr int BOX = PAGED_TILE * 128;
     static constexpr int STAGE = 2 * HALVES * BOX;
-    // Two CTAs an SM where 16 rows' sums leave room for them, else one.
-    static constexpr int NS = MT == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-    static constexpr int CTAS = MT == 1 ? 2 : 1;
-    static constexpr int R = MT * 16;
-    static constexpr int RED = NS * STAGE;                  // float [2][R][D]
-    static constexpr int ML = RED + 2 * R * D * 4;          // float [4][R][2]
-    static constexpr int DESC = ML + PG_CONS * R * 2 * 4;   // StepDesc [NS]
+    static constexpr int NS = D == 128 ? 3 : 6;
+    static constexpr int QROW = 2 * D + 16;                 // pitch: ldmatrix's 8 rows in different banks
+    static constexpr int Q = NS * STAGE;                    // [NS][PG_R][QROW]
+    static constexpr int ML = Q + NS * PG_R * QROW;         // float [4][PG_R][2]
+    static constexpr int DESC = ML + PG_CONS * PG_R * 2 * 4;
     static constexpr int BARS = (DESC + NS * (int)sizeof(StepDesc) + 7) / 8 * 8;  // full, empty [NS], join
     static constexpr int BYTES = BARS + (2 * NS + 1) * 8 + 8;
+    static_assert(PG_CONS * PG_R * D * 4 <= STAGE, "a stage holds the four warps' sums");
+    static_assert((BYTES + 1024) * PG_CTAS <= 228 * 1024, "CTAs an SM");
 };
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(PG_NT, PagedLayout<D, MT>::CTAS)
-    k_paged(const PagedArgs a, const PagedLine l, const __grid_constant__ CUtensorMap map) {
-    using LY = PagedLayout<D, MT>;
-    constexpr int KS = D / 16, NS = LY::NS, R = LY::R;
+// A piece of the walk, and the ids of its first 32 pages (lane i: page ids0 + i).
+struct Piece {
+    const int32_t *row;
+    int t0, t1, vis, head, q0, rows, lim0, limd, slot, ids0, ids;
+};
+
+// The ids of pages p .. p + 31 of a sequence that is seen up to `vis`, one a lane.
+__device__ __forceinline__ int page_ids(const PagedArgs &a, const int32_t *row, int p, int vis) {
+    p += threadIdx.x & 31;
+    int id = 0;
+    if (p <= (vis - 1) >> a.page_shift) {
+        id = row[p];
+        if (id < 0 || id >= a.num_pages) {
+            raise_error(a.err, ERR_PAGE);
+            id = 0;
+        }
+    }
+    return id;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(PG_NT, PG_CTAS)
+    k_paged(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const __grid_constant__ CUtensorMap map) {
+    using LY = PagedLayout<D>;
+    constexpr int KS = D / 16, NS = LY::NS;
     extern __shared__ __align__(1024) unsigned char pg_smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(pg_smem + LY::BARS), *empty = full + NS, *join = empty + NS;
     volatile int *abort = reinterpret_cast<volatile int *>(join + 1);
     StepDesc *desc = reinterpret_cast<StepDesc *>(pg_smem + LY::DESC);
-    float *red = reinterpret_cast<float *>(pg_smem + LY::RED);
     float *ml = reinterpret_cast<float *>(pg_smem + LY::ML);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,95 +101,109 @@ __global__ void __launch_bounds__(PG_NT, PagedLayout<D, MT>::CTAS)
         *abort = 0;
     }
     __syncthreads();
-    pdl_wait();
-    pdl_trigger();
 
     if (warp == PG_CONS) {
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
         const int box = min(1 << a.page_shift, PAGED_TILE);  // tokens of a page in one step
         PagedWalk wk;
-        wk.start(a, l, blockIdx.x);
+        // Once for its instructions, while the kernel before this one still runs; what it reads may
+        // change until the wait, and is not used.
+#pragma unroll 1
+        for (int dry = 1; dry >= 0; --dry) {
+            if (!dry) {
+                pdl_wait();
+                pdl_trigger();
+            }
+            wk.start(a, l, blockIdx.x, dry != 0);
+        }
+        // The walk is one piece ahead of the copies, so that a piece's page ids are there when its
+        // first step is.
+        auto fetch = [&](Piece &p) -> bool {
+            if (!wk.next(a, l, blockIdx.x)) return false;
+            const PagedLevel &lv = a.level[wk.s.own ? 1 : 0];
+            const int first = wk.m << l.tt_shift;
+            p.row = lv.table + (long long)wk.s.row * lv.stride;
+            p.t0 = wk.t0;
+            p.t1 = wk.t1;
+            p.vis = paged_visible(wk.s, l, wk.m);
+            p.head = wk.head;
+            p.q0 = wk.s.q0 + first;
+            p.rows = min(1 << l.tt_shift, wk.s.qn - first) << a.g_shift;
+            p.lim0 = wk.s.own ? wk.s.len - (wk.s.qn - 1 - first) : wk.s.len;
+            p.limd = wk.s.own ? 1 : 0;
+            p.slot = wk.slot < l.slots ? wk.slot : -1;
+            p.ids0 = p.t0 * PAGED_TILE >> a.page_shift;
+            p.ids = page_ids(a, p.row, p.ids0, p.vis);
+            return true;
+        };
+        Piece cur = {}, nxt = {};
+        bool have = true, go = true;
         int j = 0;
-        bool go = true;
-        while (go && wk.next(a, l, blockIdx.x)) {
-            const PagedLevel &lv = wk.s.own ? a.own : a.prefix;
-            const int32_t *row = lv.table + (long long)wk.s.row * lv.stride;
-            const int vis = paged_visible(wk.s, l.tt, wk.m);
-            int ids = 0, ids0 = 1, ids1 = 0;  // lane i: id of page ids0 + i of the sequence
-            for (int t = wk.t0; t < wk.t1; ++t, ++j) {
+        while (have && go) {
+            have = fetch(nxt);
+#pragma unroll 1
+            for (int t = cur.t0; t < cur.t1; ++t, ++j) {
                 const int k = j % NS;
-                go = *abort == 0;
-                if (go && j >= NS) go = mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort);
-                go = __all_sync(0xFFFFFFFFu, go);
+                if (j >= NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort));
                 if (!go) break;
-                const int tok0 = t * PAGED_TILE, valid = min(PAGED_TILE, vis - tok0);
-                const int pages = (valid + box - 1) / box;
-                const int p0 = tok0 >> a.page_shift;
-                if (p0 < ids0 || p0 + pages > ids1) {
-                    ids0 = p0;
-                    ids1 = p0 + 32;
-                    const int p = p0 + lane;
-                    int id = 0;
-                    if (p <= (vis - 1) >> a.page_shift) {
-                        id = row[p];
-                        if (id < 0 || id >= a.num_pages) {
-                            raise_error(a.err, ERR_PAGE);
-                            id = 0;
-                        }
-                    }
-                    ids = id;
+                const int tok0 = t * PAGED_TILE, valid = min(PAGED_TILE, cur.vis - tok0);
+                const int pages = (valid + box - 1) / box, p0 = tok0 >> a.page_shift;
+                if (p0 + pages > cur.ids0 + 32) {
+                    cur.ids0 = p0;
+                    cur.ids = page_ids(a, cur.row, p0, cur.vis);
                 }
+                const bool first = t == cur.t0;
                 if (lane == 0) {
                     StepDesc s;
-                    s.flags = (t == wk.t0 ? PG_FIRST : 0) | (t + 1 == wk.t1 ? PG_LAST : 0);
+                    s.flags = (first ? PG_FIRST : 0) | (t + 1 == cur.t1 ? PG_LAST : 0);
                     s.valid = valid;
                     s.tok0 = tok0;
-                    s.q0 = wk.s.q0 + wk.m * l.tt;
-                    s.nq = min(l.tt, wk.s.qn - wk.m * l.tt);
-                    s.head = wk.head;
-                    s.lim0 = wk.s.own ? wk.s.len - (wk.s.qn - 1 - wk.m * l.tt) : wk.s.len;
-                    s.limd = wk.s.own ? 1 : 0;
-                    s.slot = wk.slot < l.slots ? wk.slot : -1;
+                    s.rows = cur.rows;
+                    s.lim0 = cur.lim0;
+                    s.limd = cur.limd;
+                    s.slot = cur.slot;
                     if (s.slot < 0) raise_error(a.err, ERR_PAGE);
                     desc[k] = s;
-                    mbar_expect_tx(&full[k], (uint32_t)(pages * box * 4 * D));
+                    mbar_expect_tx(&full[k], (uint32_t)(pages * box * 4 * D + (first ? cur.rows * 2 * D : 0)));
                 }
                 __syncwarp();
-                const int id = __shfl_sync(0xFFFFFFFFu, ids, (p0 + lane - ids0) & 31);
+                const int id = __shfl_sync(0xFFFFFFFFu, cur.ids, (p0 + lane - cur.ids0) & 31);
                 if (lane < pages) {
-                    // page ids0 + i holds tokens tok0 + lane * box ..: a page of more than one step is
-                    // read at the step's offset in it
-                    const int y = (((id * a.hkv + wk.head) << a.page_shift) + ((tok0 + lane * box) & ((1 << a.page_shift) - 1)));
+                    // a page of more than one step is read at the step's offset in it
+                    const int y = (((id * a.hkv + cur.head) << a.page_shift) + ((tok0 + lane * box) & ((1 << a.page_shift) - 1)));
                     unsigned char *st = pg_smem + (size_t)k * LY::STAGE + lane * box * 128;
 #pragma unroll
                     for (int b = 0; b < 2 * LY::HALVES; ++b) tma_load_2d(st + b * LY::BOX, &map, b * 64, y, &full[k]);
                 }
+                if (first && lane < cur.rows) {
+                    const int jj = lane >> a.g_shift, hh = (cur.head << a.g_shift) + lane - (jj << a.g_shift);
+                    bulk_g2s(pg_smem + LY::Q + (k * PG_R + lane) * LY::QROW, a.q + (cur.q0 + jj) * a.q_ts + hh * a.q_hs, 2 * D, &full[k]);
+                }
                 __syncwarp();
             }
+            cur = nxt;
         }
         if (go) {  // tell the consumers that the run is over
             const int k = j % NS;
-            if (j >= NS) go = mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort);
+            if (j >= NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort));
             if (go && lane == 0) {
                 desc[k].flags = PG_END;
                 mbar_arrive(&full[k]);
             }
         }
-        if (!go) {
+        if (!go && lane == 0) {
             // A wait ran out.  Let the copies of this CTA land before it exits: the steps j - NS ..
             // j - 1 are the ones that may be in flight.
-            if (lane == 0) {
-                *abort = 1;
-                raise_error(a.err, ERR_TIMEOUT);
-                for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1));
-            }
+            *abort = 1;
+            raise_error(a.err, ERR_TIMEOUT);
+            for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1));
         }
         __syncwarp();
     } else {
-        const int g = lane >> 2, t = lane & 3, mi = lane >> 3, ri = lane & 7;
-        uint32_t qf[MT][KS][4];
-        float o[MT][D / 8][4], mx[MT][2], sum[MT][2];
-        int lim[MT][2];
+        const int g = lane >> 2, t = lane & 3, mi = lane >> 3, ri = lane & 7, w0 = warp * 16;
+        uint32_t qf[KS][4];
+        float o[D / 8][4], mx[2], sum[2];
+        int lim[2];
         int joins = 0;
         auto cons_sync = [&]() -> bool {
             __syncwarp();
@@ -177,222 +212,184 @@ __global__ void __launch_bounds__(PG_NT, PagedLayout<D, MT>::CTAS)
             ++joins;
             return __all_sync(0xFFFFFFFFu, ok);
         };
-        for (int j = 0;; ++j) {
-            const int k = j % NS;
-            bool ok = *abort == 0 && mbar_wait_or_abort(&full[k], (uint32_t)((j / NS) & 1), abort);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
-                if (lane == 0) {
-                    *abort = 1;
-                    raise_error(a.err, ERR_TIMEOUT);
-                }
-                break;
-            }
-            const StepDesc s = desc[k];
-            if (s.flags & PG_END) break;
-            if (s.flags & PG_FIRST) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = mt * 16 + g + 8 * e, jj = r / a.G, hh = r - jj * a.G;
-                        const bool real = jj < s.nq;
-                        lim[mt][e] = real ? s.lim0 + s.limd * jj : 0;
-                        mx[mt][e] = -INFINITY;
-                        sum[mt][e] = 0.0f;
-                        const uint16_t *qr = a.q + (long long)(s.q0 + (real ? jj : 0)) * a.q_ts + (long long)(s.head * a.G + hh) * a.q_hs;
-#pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            qf[mt][ks][e] = real ? *reinterpret_cast<const uint32_t *>(qr + ks * 16 + 2 * t) : 0u;
-                            qf[mt][ks][2 + e] = real ? *reinterpret_cast<const uint32_t *>(qr + ks * 16 + 8 + 2 * t) : 0u;
-                        }
+        // Round -1 runs a step over whatever the first slot holds, for its instructions: a kernel starts
+        // with cold instruction caches, and they would else be fetched when the first step has arrived
+        // instead of while it is on its way.  (No copy has been started into V's part of a slot that the
+        // round could write: valid is 64.)
+        for (int j = -1;; ++j) {
+            const int k = j < 0 ? 0 : j % NS;
+            StepDesc s = {PG_FIRST, PAGED_TILE, 0, 0, 0, 0, -1};
+            if (j >= 0) {
+                const bool ok = mbar_wait_or_abort(&full[k], (uint32_t)((j / NS) & 1), abort);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    if (lane == 0) {
+                        *abort = 1;
+                        raise_error(a.err, ERR_TIMEOUT);
                     }
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+                    break;
                 }
+                s = desc[k];
+                if (s.flags & PG_END) break;
             }
-            const int w0 = warp * 16;
+            unsigned char *st = pg_smem + (size_t)k * LY::STAGE;
+            if (s.flags & PG_FIRST) {
+                const uint32_t qb = smem_addr(pg_smem + LY::Q) + (k * PG_R + (mi & 1) * 8 + ri) * LY::QROW + (mi >> 1) * 16;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) ldsm_x4(qf[ks], qb + ks * 32);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = g + 8 * e;
+                    lim[e] = r < s.rows ? s.lim0 + s.limd * (r >> a.g_shift) : 0;
+                    mx[e] = -INFINITY;
+                    sum[e] = 0.0f;
+                }
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+            }
             if (w0 < s.valid) {
-                unsigned char *st = pg_smem + (size_t)k * LY::STAGE;
                 const uint32_t kb = smem_addr(st), vb = kb + LY::HALVES * LY::BOX;
                 if (w0 + 16 > s.valid) {
                     // V rows that nothing sees may hold anything, NaN too: a weight of 0 would keep it
+#pragma unroll 1
                     for (int r = s.valid; r < w0 + 16; ++r)
                         if (lane < 8 * LY::HALVES)
                             *reinterpret_cast<uint4 *>(st + (LY::HALVES + (lane >> 3)) * LY::BOX + r * 128 + (lane & 7) * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
                     __syncwarp();
                 }
-                float sc[MT][2][4];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sc[mt][e >> 2][e & 3] = 0.0f;
+                float sc[2][4] = {}, sd[2][4] = {};  // even and odd k-steps: shorter chains
                 {
                     const int r = w0 + (mi >> 1) * 8 + ri;
+                    uint32_t b[KS][4];
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        uint32_t b[4];
-                        ldsm_x4(b, kb + (ks / 4) * LY::BOX + r * 128 + ((((ks % 4) * 2 + (mi & 1)) ^ (r & 7)) << 4));
+                    for (int ks = 0; ks < KS; ++ks)
+                        ldsm_x4(b[ks], kb + (ks / 4) * LY::BOX + r * 128 + ((((ks % 4) * 2 + (mi & 1)) ^ (r & 7)) << 4));
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            T::mma(sc[mt][0], qf[mt][ks], b[0], b[1]);
-                            T::mma(sc[mt][1], qf[mt][ks], b[2], b[3]);
-                        }
+                    for (int ks = 0; ks < KS; ks += 2) {
+                        T::mma(sc[0], qf[ks], b[ks][0], b[ks][1]);
+                        T::mma(sc[1], qf[ks], b[ks][2], b[ks][3]);
+                        T::mma(sd[0], qf[ks + 1], b[ks + 1][0], b[ks + 1][1]);
+                        T::mma(sd[1], qf[ks + 1], b[ks + 1][2], b[ks + 1][3]);
                     }
                 }
-                uint32_t pf[MT][4];
+                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float top[2] = {-INFINITY, -INFINITY};
+                for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = s.tok0 + w0 + nt * 8 + 2 * t + (e & 1);
+                        float x = (sc[nt][e] + sd[nt][e]) * a.scale_log2;
+                        x = tok < lim[e >> 1] ? x : -INFINITY;
+                        sc[nt][e] = x;
+                        top[e >> 1] = fmaxf(top[e >> 1], x);
+                    }
+                bool rises = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tok = s.tok0 + w0 + nt * 8 + 2 * t + (e & 1);
-                            float x = sc[mt][nt][e] * a.scale_log2;
-                            x = tok < lim[mt][e >> 1] ? x : -INFINITY;
-                            sc[mt][nt][e] = x;
-                            top[e >> 1] = fmaxf(top[e >> 1], x);
-                        }
-                    bool rises = false;
+                for (int e = 0; e < 2; ++e) {
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2)) - T::SHIFT;
+                    rises |= top[e] > mx[e];
+                }
+                if (__any_sync(0xFFFFFFFFu, rises)) {
+                    float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
-                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2));
-                        rises |= top[e] > mx[mt][e];
-                    }
-                    if (__any_sync(0xFFFFFFFFu, rises)) {
-                        float f[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float m = fmaxf(mx[mt][e], top[e]);
-                            f[e] = m == mx[mt][e] ? 1.0f : exp2_fast(mx[mt][e] - m);  // (-inf: nothing summed yet)
-                            mx[mt][e] = m;
-                            sum[mt][e] *= f[e];
-                        }
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            o[mt][n][0] *= f[0];
-                            o[mt][n][1] *= f[0];
-                            o[mt][n][2] *= f[1];
-                            o[mt][n][3] *= f[1];
-                        }
+                        const float m = fmaxf(mx[e], top[e]);
+                        f[e] = m == mx[e] ? 1.0f : exp2_fast(mx[e] - m);  // (-inf: nothing summed yet)
+                        mx[e] = m;
+                        sum[e] *= f[e];
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float m = mx[mt][e] == -INFINITY ? 0.0f : mx[mt][e];  // a row that sees nothing so far
-                        float p[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            p[i] = exp2_fast(sc[mt][i >> 1][2 * e + (i & 1)] - m);
-                            sum[mt][e] += p[i];
-                        }
-                        pf[mt][e] = T::pack(p[0], p[1]);
-                        pf[mt][2 + e] = T::pack(p[2], p[3]);
+                    for (int n = 0; n < D / 8; ++n) {
+                        o[n][0] *= f[0];
+                        o[n][1] *= f[0];
+                        o[n][2] *= f[1];
+                        o[n][3] *= f[1];
                     }
+                }
+                uint32_t pf[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float m = mx[e] == -INFINITY ? 0.0f : mx[e];  // a row that sees nothing so far
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p[i] = exp2_fast(sc[i >> 1][2 * e + (i & 1)] - m);
+                        sum[e] += p[i];
+                    }
+                    pf[e] = T::pack(p[0], p[1]);
+                    pf[2 + e] = T::pack(p[2], p[3]);
                 }
                 const int r = w0 + (mi & 1) * 8 + ri;
 #pragma unroll
-                for (int c = 0; c < KS; ++c) {
-                    uint32_t b[4];
-                    ldsm_x4_t(b, vb + (c / 4) * LY::BOX + r * 128 + ((((c % 4) * 2 + (mi >> 1)) ^ (r & 7)) << 4));
+                for (int c0 = 0; c0 < KS; c0 += 4) {
+                    uint32_t b[4][4];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        T::mma(o[mt][2 * c], pf[mt], b[0], b[1]);
-                        T::mma(o[mt][2 * c + 1], pf[mt], b[2], b[3]);
+                    for (int c = 0; c < 4; ++c)
+                        ldsm_x4_t(b[c], vb + (c0 / 4) * LY::BOX + r * 128 + (((c * 2 + (mi >> 1)) ^ (r & 7)) << 4));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        T::mma(o[2 * (c0 + c)], pf, b[c][0], b[c][1]);
+                        T::mma(o[2 * (c0 + c) + 1], pf, b[c][2], b[c][3]);
                     }
                 }
-                fence_proxy_async_smem();  // generic accesses before the slot's next copy
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[k]);
+            if (j < 0) continue;
 
             if (s.flags & PG_LAST) {
-                // Join the four warps' states: each scales its sums to the common maximum, then
-                // 1 -> 0 and 3 -> 2, then 2 -> 0.
+                // Join the four warps' states: each scales its sums to the common maximum and lays
+                // them in the slot, and all threads add the four and write the partial.
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int e = 0; e < 2; ++e) {
+                    sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
+                    sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
+                    if (t == 0) *reinterpret_cast<float2 *>(ml + (warp * PG_R + g + 8 * e) * 2) = make_float2(mx[e], sum[e]);
+                }
+                if (!cons_sync()) break;  // and no warp reads the slot's K and V any more
+                float *buf = reinterpret_cast<float *>(st);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sum[mt][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[mt][e], 1);
-                        sum[mt][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[mt][e], 2);
-                        if (t == 0) {
-                            float *p = ml + (warp * R + mt * 16 + g + 8 * e) * 2;
-                            p[0] = mx[mt][e];
-                            p[1] = sum[mt][e];
-                        }
-                    }
-                if (!cons_sync()) break;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = g + 8 * e;
+                    float m = -INFINITY, z = 0.0f;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                    for (int w = 0; w < PG_CONS; ++w) m = fmaxf(m, ml[(w * PG_R + r) * 2]);
+                    const float ms = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = mt * 16 + g + 8 * e;
-                        float m = -INFINITY, z = 0.0f;
-#pragma unroll
-                        for (int w = 0; w < PG_CONS; ++w) m = fmaxf(m, ml[(w * R + r) * 2]);
-                        const float ms = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-                        for (int w = 0; w < PG_CONS; ++w) z += ml[(w * R + r) * 2 + 1] * exp2_fast(ml[(w * R + r) * 2] - ms);
-                        const float f = exp2_fast(mx[mt][e] - ms);
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            o[mt][n][2 * e] *= f;
-                            o[mt][n][2 * e + 1] *= f;
-                        }
-                        mx[mt][e] = m;
-                        sum[mt][e] = z;
-                    }
-                auto put = [&](float *buf) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int w = 0; w < PG_CONS; ++w) z += ml[(w * PG_R + r) * 2 + 1] * exp2_fast(ml[(w * PG_R + r) * 2] - ms);
+                    if (r < s.rows) {
+                        const float f = exp2_fast(mx[e] - ms);
 #pragma unroll
                         for (int n = 0; n < D / 8; ++n)
-                            reinterpret_cast<float4 *>(buf)[(mt * (D / 8) + n) * 32 + lane] =
-                                make_float4(o[mt][n][0], o[mt][n][1], o[mt][n][2], o[mt][n][3]);
-                };
-                auto add = [&](const float *buf) {
+                            *reinterpret_cast<float2 *>(buf + (warp * PG_R + r) * D + ((n * 8 + 2 * t) ^ (g << 3))) =
+                                make_float2(o[n][2 * e] * f, o[n][2 * e + 1] * f);
+                        if (t == 0 && warp == 0 && s.slot >= 0)
+                            *reinterpret_cast<float2 *>(l.part_ml + ((long long)s.slot * PG_R + r) * 2) = make_float2(m, z);
+                    }
+                }
+                if (!cons_sync()) break;
+                if (s.slot >= 0) {
+                    float *po = l.part_o + (long long)s.slot * PG_R * D;
+#pragma unroll 1
+                    for (int x = tid * 4; x < s.rows * D; x += PG_CONS * 32 * 4) {
+                        const int y = x ^ (((x / D) & 7) << 3);  // as laid: 8 channels' groups turned by the row
+                        float4 v = *reinterpret_cast<const float4 *>(buf + y);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            const float4 v = reinterpret_cast<const float4 *>(buf)[(mt * (D / 8) + n) * 32 + lane];
-                            o[mt][n][0] += v.x;
-                            o[mt][n][1] += v.y;
-                            o[mt][n][2] += v.z;
-                            o[mt][n][3] += v.w;
+                        for (int w = 1; w < PG_CONS; ++w) {
+                            const float4 u = *reinterpret_cast<const float4 *>(buf + w * PG_R * D + y);
+                            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
                         }
-                };
-                if (warp & 1) put(red + (warp >> 1) * R * D);
-                if (!cons_sync()) break;
-                if (!(warp & 1)) add(red + (warp >> 1) * R * D);
-                if (!cons_sync()) break;
-                if (warp == 2) put(red);
-                if (!cons_sync()) break;
-                if (warp == 0) {
-                    add(red);
-                    if (s.slot >= 0) {
-                        const int rows = s.nq * a.G;
-                        float *po = l.part_o + (long long)s.slot * (l.tt * a.G) * D;
-                        float *pm = l.part_ml + (long long)s.slot * (l.tt * a.G) * 2;
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int r = mt * 16 + g + 8 * e;
-                                if (r >= rows) continue;
-#pragma unroll
-                                for (int n = 0; n < D / 8; ++n)
-                                    *reinterpret_cast<float2 *>(po + r * D + n * 8 + 2 * t) =
-                                        make_float2(o[mt][n][2 * e], o[mt][n][2 * e + 1]);
-                                if (t == 0) *reinterpret_cast<float2 *>(pm + r * 2) = make_float2(mx[mt][e], sum[mt][e]);
-                            }
+                        *reinterpret_cast<float4 *>(po + x) = v;
                     }
                 }
             }
+            fence_proxy_async_smem();  // generic accesses before the slot's next copy
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[k]);
         }
+        // The caller's stream may go on only when the launch before this one is done.
+        pdl_wait();
     }
     __syncthreads();
 }
@@ -402,96 +399,121 @@ __global__ void __launch_bounds__(PG_NT, PagedLayout<D, MT>::CTAS)
 __device__ __forceinline__ int last_at_most(const int32_t *start, int n, int x) {
     int c = 0;
 #pragma unroll 4
-    for (int i = threadIdx.x & 31; i <= n; i += 32) c += start[i] <= x ? 1 : 0;
+    for (int i = threadIdx.x & 31; i <= n; i += 32) c += __ldcg(start + i) <= x ? 1 : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
     return c - 1;
 }
 
 constexpr int PM_NT = 128;
+constexpr int PM_FIRST = 1024;  // blocks that are there before the partials are
 
 template <typename T, int D>
-__global__ void __launch_bounds__(PM_NT) k_paged_merge(const PagedArgs a, const PagedLine l0, const PagedLine l1) {
+__global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLines lines) {
     constexpr int V = D / 32;  // channels a lane holds
-    pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int hq = a.hkv * a.G;
+    const int hq = a.hkv << a.g_shift;
     const long long row = (long long)blockIdx.x * (PM_NT / 32) + (threadIdx.x >> 5);
     if (row >= (long long)a.q_tokens * hq) return;
-    const int t = (int)(row / hq), hh = (int)(row - (long long)t * hq), head = hh / a.G, g = hh - head * a.G;
-    const int s = a.q_start ? last_at_most(a.q_start, a.seqs, t) : t;
-    const int grp = a.prefix.rows == 0 ? -1 : a.group_start ? last_at_most(a.group_start, a.prefix.rows, s) : 0;
+    const int t = (int)(row / hq), hh = (int)(row - (long long)t * hq), head = hh >> a.g_shift, g = hh - (head << a.g_shift);
+    // The first blocks twice: once for the instructions, while the partials are still being made (what
+    // it reads then may change and is not used, and every index is within its buffer whatever the
+    // records hold).
+#pragma unroll 1
+    for (int pass = blockIdx.x < PM_FIRST ? 0 : 1; pass < 2; ++pass) {
+        if (pass) {
+            pdl_wait();
+            pdl_trigger();
+        }
+        const int s = a.q_start ? last_at_most(a.q_start, a.seqs, t) : t;
 
-    float m = -INFINITY, z = 0.0f, acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    // Join a state (maximum, sum, weighted values) whose values are at src, scaled by their sum's unit.
-    auto join = [&](float m2, float z2, const float *src) {
-        if (z2 == 0.0f) return;  // it summed nothing
-        const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.0f : mn;
-        const float f = exp2_fast(m - ms), f2 = exp2_fast(m2 - ms);
-        z = z * f + z2 * f2;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = acc[i] * f + src[i] * f2;
-        m = mn;
-    };
-#pragma unroll
-    for (int x = 0; x < PAGED_LINES; ++x) {
-        const PagedLine &l = x ? l1 : l0;
+        // Where the row's partials are: of its prefix, then of its own pages.
+        const float *po[2] = {}, *pm[2] = {};
+        int count[2] = {0, 0}, rows[2] = {0, 0};  // a slot's rows
+        bool grouped[2] = {false, false};
 #pragma unroll
         for (int own = 0; own < 2; ++own) {
-            if (!(own ? l.with_own : l.with_prefix)) continue;
-            const int r = own ? s : grp;
-            if (r < 0 || r >= (own ? a.own.rows : a.prefix.rows)) continue;
-            const int i = r + (own && l.with_prefix ? a.prefix.rows : 0);
+            const int at = lines.l[1].with[own] ? 1 : 0;
+            const PagedLine &l = lines.l[at];
+            if (!l.with[own]) continue;
+            const int r = own ? s : a.group_start ? last_at_most(a.group_start, a.level[0].rows, s) : 0;
+            if (r < 0 || r >= a.level[own].rows) continue;
+            const int i = r + (own && l.with[0] ? a.level[0].rows : 0);
+            const int per = __ldcg(l.rec).x;
+            const int2 before = __ldcg(l.rec + 1 + i);
             bool bad = false;
             const PagedSeg sg = paged_segment(a, l, i, bad);
             const int j = t - sg.q0;
-            if (j < 0 || j >= sg.qn) continue;
-            const int nt = paged_row_tiles(sg, l.tt), mt = j / l.tt;
-            const int steps = paged_steps(sg, l, mt);
+            if (j < 0 || j >= sg.qn || per <= 0) continue;  // (per 0: a bad segment, nothing was done)
+            const int nt = paged_row_tiles(sg, l), mt = j >> l.tt_shift, steps = paged_steps(sg, l, mt);
             if (steps == 0) continue;
-            const int per = l.rec[0].x;
-            if (per == 0) continue;  // a bad segment: nothing was done
-            const int2 before = l.rec[1 + i];
             const int w0 = before.x + head * paged_steps_before(sg, l, nt) + paged_steps_before(sg, l, mt);
-            const int u = before.y + head * nt + mt;
-            const int in = (j - mt * l.tt) * a.G + g, R = l.tt * a.G;
-            const int c0 = w0 / per, c1 = (w0 + steps - 1) / per;
+            const int c0 = (unsigned)w0 / (unsigned)per, c1 = (unsigned)(w0 + steps - 1) / (unsigned)per;
+            const int in = ((j - (mt << l.tt_shift)) << a.g_shift) + g;
+            const int slot = clampi(c0 + before.y + head * nt + mt, 0, l.slots - 1);
+            count[own] = clampi(c1 - c0 + 1, 0, l.slots - slot);
+            rows[own] = 1 << (l.tt_shift + a.g_shift);
+            grouped[own] = l.grouped != 0;
+            po[own] = l.part_o + (long long)slot * rows[own] * D + (l.grouped ? (in >> 2) * (D * 4) + (in & 3) * 4 : in * D);
+            pm[own] = l.part_ml + ((long long)slot * rows[own] + in) * 2;
+        }
+        float prior = -INFINITY;
+        if (a.prior_lse) prior = __ldcg(a.prior_lse + row) * 1.4426950408889634f;
+
+        // 32 partials a turn, a lane each: its state, and where its values are.  A partial whose sum is 0
+        // summed nothing, and its values are not used.
+        const int n = pass ? count[0] + count[1] : min(count[0] + count[1], 32);
+        const int flat = lane * V, quad = (lane * V / 4) * 16 + lane * V % 4;  // this lane's channels in either order
+        float m = prior, z = 0.0f, acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+        if (m != -INFINITY) {
+            z = lane == 0 ? 1.0f : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = __ldcg(a.prior_o + row * D + flat + i);
+        }
+#pragma unroll 1
+        for (int x0 = 0; x0 < n; x0 += 32) {
+            const int x = x0 + lane, v = x < count[0] ? 0 : 1, k = x - (v ? count[0] : 0);
+            float2 mine = make_float2(-INFINITY, 0.0f);
+            unsigned long long at = 0;
+            if (x < n) {
+                mine = __ldcg(reinterpret_cast<const float2 *>((v ? pm[1] : pm[0]) + (long long)k * (v ? rows[1] : rows[0]) * 2));
+                at = reinterpret_cast<unsigned long long>((v ? po[1] : po[0]) + (long long)k * (v ? rows[1] : rows[0]) * D);
+            }
+            const unsigned in_quads = __ballot_sync(0xFFFFFFFFu, v ? grouped[1] : grouped[0]);
+            const float mn = fmaxf(m, warp_max(mine.x)), ms = mn == -INFINITY ? 0.0f : mn;
+            const float f = exp2_fast(m - ms), w = exp2_fast(mine.x - ms);
+            z = z * f + (mine.y == 0.0f ? 0.0f : mine.y * w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] *= f;
+            m = mn;
+            const unsigned some = __ballot_sync(0xFFFFFFFFu, mine.y != 0.0f);
+            const int c = min(32, n - x0);
 #pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-                const long long at = c + u;
-                if (at >= l.slots) break;
-                const float2 mz = *reinterpret_cast<const float2 *>(l.part_ml + (at * R + in) * 2);
-                float v[V];
-                const float *src = l.part_o + at * R * D +
-                                   (l.grouped ? (lane * V / 4) * R * 4 + in * 4 + lane * V % 4 : in * D + lane * V);
+            for (int y = 0; y < c; ++y) {
+                const float wy = __shfl_sync(0xFFFFFFFFu, w, y);
+                const float *src = reinterpret_cast<const float *>(__shfl_sync(0xFFFFFFFFu, at, y)) + ((in_quads >> y & 1) ? quad : flat);
+                float u[V];
                 if (V == 4) {
-                    const float4 q = *reinterpret_cast<const float4 *>(src);
-                    v[0] = q.x; v[1] = q.y; v[V - 2] = q.z; v[V - 1] = q.w;
+                    const float4 q = __ldcg(reinterpret_cast<const float4 *>(src));
+                    u[0] = q.x; u[1] = q.y; u[V - 2] = q.z; u[V - 1] = q.w;
                 } else {
-                    const float2 q = *reinterpret_cast<const float2 *>(src);
-                    v[0] = q.x; v[1] = q.y;
+                    const float2 q = __ldcg(reinterpret_cast<const float2 *>(src));
+                    u[0] = q.x; u[1] = q.y;
                 }
-                join(mz.x, mz.y, v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = (some >> y & 1) ? fmaf(u[i], wy, acc[i]) : acc[i];
             }
         }
-    }
-    if (a.prior_lse) {
-        const float pl = a.prior_lse[row];
-        if (pl != -INFINITY) {
-            float v[V];
+        z = warp_sum(z);
+        if (!pass) continue;
+        const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row * D + lane * V);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = a.prior_o[row * D + lane * V + i];
-            join(pl * 1.4426950408889634f, 1.0f, v);
-        }
+        for (int i = 0; i < V / 2; ++i) dst[i] = T::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+        if (a.lse && lane == 0) a.lse[row] = z == 0.0f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
     }
-    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row * D + lane * V);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) dst[i] = T::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (a.lse && lane == 0) a.lse[row] = z == 0.0f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
 }
 
 }  // namespace
@@ -513,27 +535,24 @@ cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long l
 
 cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, int dtype, int d,
                          cudaStream_t s) {
-    const int mt = l.tt * a.G / 16;
-#define VERKV_PAGED(TT, DT, DD, MM)                                                            \
-    if (dtype == DT && d == DD && mt == MM) {                                                  \
-        const size_t smem = PagedLayout<DD, MM>::BYTES;                                        \
-        const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD, MM>, smem);            \
-        if (e != cudaSuccess) return e;                                                        \
-        return launch_pdl(k_paged<TT, DD, MM>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, map); \
+#define VERKV_PAGED(TT, DT, DD)                                                            \
+    if (dtype == DT && d == DD) {                                                          \
+        const size_t smem = PagedLayout<DD>::BYTES;                                        \
+        const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD>, smem);            \
+        if (e != cudaSuccess) return e;                                                    \
+        return launch_pdl(k_paged<TT, DD>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, map); \
     }
-    VERKV_PAGED(PgBf16, VERKV_BF16, 128, 1) VERKV_PAGED(PgBf16, VERKV_BF16, 128, 2)
-    VERKV_PAGED(PgBf16, VERKV_BF16, 64, 1) VERKV_PAGED(PgBf16, VERKV_BF16, 64, 2)
-    VERKV_PAGED(PgF16, VERKV_F16, 128, 1) VERKV_PAGED(PgF16, VERKV_F16, 128, 2)
-    VERKV_PAGED(PgF16, VERKV_F16, 64, 1) VERKV_PAGED(PgF16, VERKV_F16, 64, 2)
+    VERKV_PAGED(PgBf16, VERKV_BF16, 128) VERKV_PAGED(PgBf16, VERKV_BF16, 64)
+    VERKV_PAGED(PgF16, VERKV_F16, 128) VERKV_PAGED(PgF16, VERKV_F16, 64)
 #undef VERKV_PAGED
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLine *lines, int dtype, int d, cudaStream_t s) {
-    const long long rows = (long long)a.q_tokens * a.hkv * a.G, blocks = (rows + PM_NT / 32 - 1) / (PM_NT / 32);
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLines &lines, int dtype, int d, cudaStream_t s) {
+    const long long rows = (long long)a.q_tokens * (a.hkv << a.g_shift), blocks = (rows + PM_NT / 32 - 1) / (PM_NT / 32);
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
 #define VERKV_PM(TT, DT, DD) \
-    if (dtype == DT && d == DD) return launch_pdl(k_paged_merge<TT, DD>, dim3((unsigned)blocks), dim3(PM_NT), 0, s, a, lines[0], lines[1]);
+    if (dtype == DT && d == DD) return launch_pdl(k_paged_merge<TT, DD>, dim3((unsigned)blocks), dim3(PM_NT), 0, s, a, lines);
     VERKV_PM(PgBf16, VERKV_BF16, 128) VERKV_PM(PgBf16, VERKV_BF16, 64)
     VERKV_PM(PgF16, VERKV_F16, 128) VERKV_PM(PgF16, VERKV_F16, 64)
 #undef VERKV_PM

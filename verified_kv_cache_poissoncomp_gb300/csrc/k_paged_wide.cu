@@ -59,8 +59,8 @@ struct WideLayout {
     static constexpr int ML = RING + NS * SLOT;                          // float [2][128][2]
     static constexpr int PIECES = ML + 2 * 128 * 2 * 4;                  // PieceDesc [PW_PIECES]
     static constexpr int BARS = (PIECES + PW_PIECES * (int)sizeof(PieceDesc) + 7) / 8 * 8;
-    // full, empty [NS]; piece [PW_PIECES]; s_full, p_full [2]; q_full, o_full, ml_full; drain, turn [2]
-    static constexpr int NBARS = 2 * NS + PW_PIECES + 4 + 7;
+    // full, empty [NS]; piece [PW_PIECES]; s_full, h_full, p_full [2]; q_full, o_full, ml_full; drain, turn [2]
+    static constexpr int NBARS = 2 * NS + PW_PIECES + 6 + 7;
     static constexpr int BYTES = BARS + NBARS * 8 + 16;
 };
 
@@ -68,12 +68,12 @@ template <typename T>
 struct Weights;
 template <>
 struct Weights<PgBf16> {
-    static constexpr float SHIFT = 0.0f, SLACK = 8.0f;
+    static constexpr float SLACK = 8.0f;
     static constexpr bool BF = true;
 };
 template <>
 struct Weights<PgF16> {
-    static constexpr float SHIFT = 8.0f, SLACK = 6.0f;
+    static constexpr float SLACK = 6.0f;
     static constexpr bool BF = false;
 };
 
@@ -98,13 +98,13 @@ __device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_fl
 
 template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(PW_NT, 1)
-    k_paged_wide(const PagedArgs a, const PagedLine l, const int wait_first, const __grid_constant__ CUtensorMap map) {
+    k_paged_wide(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int wait_first, const __grid_constant__ CUtensorMap map) {
     using LY = WideLayout<D, TILES>;
     using W = Weights<T>;
     constexpr int NS = LY::NS, R = LY::R;
     extern __shared__ __align__(1024) unsigned char pw_smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(pw_smem + LY::BARS), *empty = full + NS, *piece = empty + NS;
-    uint64_t *s_full = piece + PW_PIECES, *p_full = s_full + 2, *q_full = p_full + 2, *o_full = q_full + 1;
+    uint64_t *s_full = piece + PW_PIECES, *h_full = s_full + 2, *p_full = h_full + 2, *q_full = p_full + 2, *o_full = q_full + 1;
     uint64_t *ml_full = o_full + 1, *drain = ml_full + 1, *turn = drain + 2;
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(turn + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_at + 1);
@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
         for (int k = 0; k < PW_PIECES; ++k) mbar_init(&piece[k], 1);
         for (int k = 0; k < 2; ++k) {
             mbar_init(&s_full[k], 1);
+            mbar_init(&h_full[k], 4);
             mbar_init(&p_full[k], 4);
         }
         mbar_init(q_full, 8);
@@ -138,11 +139,8 @@ __global__ void __launch_bounds__(PW_NT, 1)
     tcgen05_after_sync();
     const uint32_t tm = *tmem_at;
     // S (and P over it) of chain i in columns 128 i .., O in 256 + 128 i ..
-    if (wait_first) pdl_wait();
-    pdl_trigger();
-
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait_or_abort(bar, parity & 1u, abort);
+        const bool ok = paged_wait(bar, parity, abort);
         if (__all_sync(0xFFFFFFFFu, ok)) return true;
         if (lane == 0) {
             *abort = 1;
@@ -153,15 +151,25 @@ __global__ void __launch_bounds__(PW_NT, 1)
 
     if (warp == PW_COPY) {
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
-        const int box = min(1 << a.page_shift, PAGED_WIDE_TILE);
+        // Nothing of the caller's is read before the kernel ahead is done -- but for the walk, once, for
+        // its instructions; what it reads may change until the wait, and is not used.  The other warps
+        // touch the caller's data only after the first piece that this one announces.
         PagedWalk wk;
-        wk.start(a, l, blockIdx.x);
+#pragma unroll 1
+        for (int dry = 1; dry >= 0; --dry) {
+            if (!dry) {
+                if (wait_first) pdl_wait();
+                pdl_trigger();
+            }
+            wk.start(a, l, blockIdx.x, dry != 0);
+        }
+        const int box = min(1 << a.page_shift, PAGED_WIDE_TILE);
         int j = 0, np = 0;  // slots and pieces so far
         bool go = true;
         while (go && wk.next(a, l, blockIdx.x)) {
-            const PagedLevel &lv = wk.s.own ? a.own : a.prefix;
+            const PagedLevel &lv = a.level[wk.s.own ? 1 : 0];
             const int32_t *row = lv.table + (long long)wk.s.row * lv.stride;
-            const int vis = paged_visible(wk.s, l.tt, wk.m);
+            const int vis = paged_visible(wk.s, l, wk.m);
             int ids = 0, ids0 = 1, ids1 = 0;  // lane i: id of page ids0 + i of the sequence
             for (int t = wk.t0; t < wk.t1 && go; ++t) {
                 const int tok0 = t * PAGED_WIDE_TILE, valid = min(PAGED_WIDE_TILE, vis - tok0);
@@ -195,10 +203,10 @@ __global__ void __launch_bounds__(PW_NT, 1)
                             s.steps = wk.t1 - wk.t0;
                             s.tok0 = tok0;
                             s.vis = vis;
-                            s.q0 = wk.s.q0 + wk.m * l.tt;
-                            s.nq = min(l.tt, wk.s.qn - wk.m * l.tt);
+                            s.q0 = wk.s.q0 + (wk.m << l.tt_shift);
+                            s.nq = min(1 << l.tt_shift, wk.s.qn - (wk.m << l.tt_shift));
                             s.head = wk.head;
-                            s.lim0 = wk.s.own ? wk.s.len - (wk.s.qn - 1 - wk.m * l.tt) : wk.s.len;
+                            s.lim0 = wk.s.own ? wk.s.len - (wk.s.qn - 1 - (wk.m << l.tt_shift)) : wk.s.len;
                             s.limd = wk.s.own ? 1 : 0;
                             s.slot = wk.slot < l.slots ? wk.slot : -1;
                             if (s.slot < 0) raise_error(a.err, ERR_PAGE);
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
             const uint32_t st = tm + i * 128, ot = tm + 256 + i * 128;
             auto await = [&](uint64_t *bar, uint32_t parity) -> bool {
                 if (mbar_try_wait(bar, parity & 1u)) return true;
-                if (mbar_wait_or_abort(bar, parity & 1u, abort)) return true;
+                if (paged_wait(bar, parity, abort)) return true;
                 *abort = 1;
                 raise_error(a.err, ERR_TIMEOUT);
                 return false;
@@ -312,21 +320,28 @@ __global__ void __launch_bounds__(PW_NT, 1)
                             fence_proxy_async_smem();
                         }
                         if (more && !(go = await(&full[ks], kf))) break;
-                        if (!(go = await(&p_full[i], ns))) break;
-                        ++ns;
+                        if (!(go = await(&h_full[i], ns))) break;
                     }
                     if (!(go = take())) break;
                     tcgen05_after_sync();
                     if (has) {
                         const uint64_t vd = ring + (uint32_t)(vs * (LY::SLOT >> 4));
                         const bool add = step != first;
+                        // The first half of P's tokens, while the softmax writes the second.
                         if (valid > PAGED_WIDE_TILE - 16) {
 #pragma unroll
-                            for (int x = 0; x < PAGED_WIDE_TILE / 16; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, add || x > 0);
+                            for (int x = 0; x < 4; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, add || x > 0);
+                            if (!(go = await(&p_full[i], ns))) break;
+                            tcgen05_after_sync();
+#pragma unroll
+                            for (int x = 4; x < 8; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, true);
                         } else {
+                            if (!(go = await(&p_full[i], ns))) break;
+                            tcgen05_after_sync();
 #pragma unroll 1
                             for (int x = 0; x < (valid + 15) / 16; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, add || x > 0);
                         }
+                        ++ns;
                         if (more) do_s();
                     }
                     pass();
@@ -367,13 +382,13 @@ __global__ void __launch_bounds__(PW_NT, 1)
                 if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
                 pd = pieces[np % PW_PIECES];
                 if (pd.steps == 0) break;
-                const int jj = row / a.G, hh = row - jj * a.G;
+                const int jj = row >> a.g_shift, hh = row - (jj << a.g_shift);
                 real = jj < pd.nq;
                 busy = __any_sync(0xFFFFFFFFu, real);  // a warp without rows only keeps step
                 lim = real ? pd.lim0 + pd.limd * jj : 0;
                 count = TILES == 2 ? pd.steps : (pd.steps + 1 - i) / 2;
                 // Q, swizzled as the copies are: a thread a row; with one tile the chains halve it.
-                const uint16_t *src = a.q + (long long)(pd.q0 + (real ? jj : 0)) * a.q_ts + (long long)(pd.head * a.G + hh) * a.q_hs;
+                const uint16_t *src = a.q + (long long)(pd.q0 + (real ? jj : 0)) * a.q_ts + (long long)((pd.head << a.g_shift) + hh) * a.q_hs;
                 unsigned char *dst = pw_smem + LY::Q + (TILES == 2 ? i * LY::SLOT : 0);
                 constexpr int N = TILES == 2 ? D / 8 : D / 16;
                 const int c0 = TILES == 2 ? 0 : i * N;
@@ -409,7 +424,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                     for (int x = 0; x < 4; ++x) top[x] = __uint_as_float(s[x]);
 #pragma unroll
                     for (int x = 4; x < 128; ++x) top[x & 3] = fmaxf(top[x & 3], __uint_as_float(s[x]));
-                    const float want = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c - W::SHIFT;
+                    const float want = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c - T::SHIFT;
                     if (__any_sync(0xFFFFFFFFu, want > ref + W::SLACK || (ref == -INFINITY && want != -INFINITY))) {
                         const float m = fmaxf(ref, want);
                         const float f = m == ref ? 1.0f : exp2_fast(ref - m);
@@ -442,14 +457,22 @@ __global__ void __launch_bounds__(PW_NT, 1)
                             add2(part[x & 1], u, v);
                         }
                         tmem_st32(ts + 32 * h, p);
+                        tmem_wait_st();
+                        if (h == 0 && !dry) {
+                            tcgen05_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&h_full[i]);
+                        }
                     }
-                    tmem_wait_st();
                     sum += (lo2(part[0]) + hi2(part[0])) + (lo2(part[1]) + hi2(part[1]));
                 }
                 if (dry) break;
                 tcgen05_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[i]);
+                if (lane == 0) {
+                    if (!busy) mbar_arrive(&h_full[i]);
+                    mbar_arrive(&p_full[i]);
+                }
                 ++ns;
             }
             if (dry) continue;
@@ -465,8 +488,9 @@ __global__ void __launch_bounds__(PW_NT, 1)
             if (!wait(o_full, (uint32_t)np)) break;
             tcgen05_after_sync();
             if (busy) {
-                // Partials lie [slot][4-channel group][row]: consecutive rows are written together.
-                float *po = l.part_o + (long long)max(pd.slot, 0) * R * D + row * 4;
+                // Partials lie [slot][group of 4 rows][group of 4 channels][4 rows][4]: lanes (rows) write
+                // whole sectors, and a reader of one row shares its lines with its neighbours'.
+                float *po = l.part_o + (long long)max(pd.slot, 0) * R * D + (row >> 2) * (D * 4) + (row & 3) * 4;
                 float *pm = l.part_ml + ((long long)max(pd.slot, 0) * R + row) * 2;
                 const bool put = real && pd.slot >= 0;
                 if (TILES == 2) {
@@ -477,7 +501,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                         if (put) {
 #pragma unroll
                             for (int y = 0; y < 8; ++y)
-                                *reinterpret_cast<uint4 *>(po + (long long)(x / 4 + y) * R * 4) =
+                                *reinterpret_cast<uint4 *>(po + (x / 4 + y) * 16) =
                                     make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                         }
                     }
@@ -502,7 +526,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                         if (put) {
 #pragma unroll
                             for (int y = 0; y < 8; ++y)
-                                *reinterpret_cast<uint4 *>(po + (long long)(x / 4 + y) * R * 4) =
+                                *reinterpret_cast<uint4 *>(po + (x / 4 + y) * 16) =
                                     make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                         }
                     }
@@ -518,7 +542,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     __syncthreads();
     tcgen05_after_sync();
     if (warp == PW_MMA) tmem_free(tm, 512);
-    if (!wait_first) pdl_wait();  // the launch before this one is done when this one is
+    pdl_wait();  // the launch before this one is done when this one is
 }
 
 }  // namespace
@@ -528,7 +552,7 @@ cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const C
     PagedArgs a = args;
     // a scale that rounds to 0 would make the masked logits' -infinity not a number
     if (fabsf(a.scale_log2) < FLT_MIN) a.scale_log2 = copysignf(FLT_MIN, a.scale_log2);
-    const int tiles = l.tt * a.G / 128;
+    const int tiles = (1 << (l.tt_shift + a.g_shift)) / 128;
 #define VERKV_WIDE(TT, DT, DD, NN)                                                              \
     if (dtype == DT && d == DD && tiles == NN) {                                                \
         const size_t smem = WideLayout<DD, NN>::BYTES;                                          \

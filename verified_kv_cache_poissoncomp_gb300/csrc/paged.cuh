@@ -49,13 +49,13 @@ struct PagedLevel {
 
 // One launch's share of the work.
 struct PagedLine {
-    int with_prefix, with_own;  // the segments in it: prefixes first
-    int tile;                   // tokens of a step
-    int tt;                     // query tokens of a row tile
+    int with[2];                // the levels in it: prefixes first
+    int tile_shift;             // log2 of the tokens of a step
+    int tt_shift;               // log2 of the query tokens of a row tile, tt
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
     int2 *rec;                  // {per, 0}, then {work before, units before} of each segment; per 0: no work
-    int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][d / 4][tt * G][4]
+    int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
     float *part_o;
     float *part_ml;             // [slots][tt * G][2]: running maximum (log2 units) and sum
 };
@@ -64,8 +64,8 @@ struct PagedArgs {
     const uint16_t *q;
     long long q_ts, q_hs;
     const int32_t *q_start, *group_start;
-    PagedLevel prefix, own;
-    int seqs, q_tokens, hkv, G, page_shift, num_pages;
+    PagedLevel level[2];  // of the prefixes, and of the sequences' own tokens
+    int seqs, q_tokens, hkv, g_shift, page_shift, num_pages;  // q_per_kv = 2^g_shift
     float scale_log2;  // logits are taken in units of log 2
     uint32_t *err;
     const float *prior_o, *prior_lse;
@@ -76,6 +76,7 @@ struct PagedArgs {
 constexpr int PAGED_MAX_CTAS = 512;   // of k_paged
 constexpr int PAGED_WIDE_CTAS = 256;  // of k_paged_wide
 constexpr int PAGED_TILE = 64;        // tokens of a step of k_paged
+constexpr int PAGED_ROWS = 16;        // rows of its units
 constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
 constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
 
@@ -86,7 +87,10 @@ cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorM
 // for to begin.
 cudaError_t launch_paged_wide(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype,
                               int d, cudaStream_t s);
-cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLine *lines, int dtype, int d, cudaStream_t s);
+struct PagedLines {
+    PagedLine l[PAGED_LINES];
+};
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLines &lines, int dtype, int d, cudaStream_t s);
 
 #ifdef __CUDACC__
 // ---------------------------------------------------------------------------------------------
@@ -98,57 +102,64 @@ struct PagedSeg {
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
 __device__ __forceinline__ int paged_segments(const PagedArgs &a, const PagedLine &l) {
-    return (l.with_prefix ? a.prefix.rows : 0) + (l.with_own ? a.own.rows : 0);
+    return (l.with[0] ? a.level[0].rows : 0) + (l.with[1] ? a.level[1].rows : 0);
 }
 
+// Loads that may happen before the kernel ahead is done (see PagedWalk::start, k_paged_merge) go past
+// the L1 cache, which would give the same old value again after the wait.
+//
 // Segment i.  Everything read from the device is clamped to its range, so that no later index
 // leaves the tensors; `bad` is set where that changed something.
 __device__ __forceinline__ PagedSeg paged_segment(const PagedArgs &a, const PagedLine &l, int i, bool &bad) {
     PagedSeg s;
-    const int np = l.with_prefix ? a.prefix.rows : 0;
+    const int np = l.with[0] ? a.level[0].rows : 0;
     s.own = i >= np;
     s.row = s.own ? i - np : i;
     int s0 = s.row, s1 = s.row + 1;
     if (!s.own) {
-        const int r0 = a.group_start ? a.group_start[s.row] : 0;
-        const int r1 = a.group_start ? a.group_start[s.row + 1] : a.seqs;
+        const int r0 = a.group_start ? __ldcg(a.group_start + s.row) : 0;
+        const int r1 = a.group_start ? __ldcg(a.group_start + s.row + 1) : a.seqs;
         s0 = clampi(r0, 0, a.seqs);
         s1 = clampi(r1, s0, a.seqs);
         bad |= s0 != r0 || s1 != r1 || (s.row == 0 && r0 != 0) || (s.row == np - 1 && r1 != a.seqs);
     }
-    const int r0 = a.q_start ? a.q_start[s0] : s0;
-    const int r1 = a.q_start ? a.q_start[s1] : s1;
+    const int r0 = a.q_start ? __ldcg(a.q_start + s0) : s0;
+    const int r1 = a.q_start ? __ldcg(a.q_start + s1) : s1;
     s.q0 = clampi(r0, 0, a.q_tokens);
     const int q1 = clampi(r1, s.q0, a.q_tokens);
     bad |= s.q0 != r0 || q1 != r1 || (s0 == 0 && s.q0 != 0) || (s1 == a.seqs && q1 != a.q_tokens);
     s.qn = q1 - s.q0;
-    const PagedLevel &lv = s.own ? a.own : a.prefix;
-    const int len = lv.length[s.row];
+    const PagedLevel &lv = a.level[s.own ? 1 : 0];
+    const int len = __ldcg(lv.length + s.row);
     s.len = clampi(len, 0, lv.max_length);
     bad |= s.len != len;
     return s;
 }
 
-__device__ __forceinline__ int paged_row_tiles(const PagedSeg &s, int tt) { return (s.qn + tt - 1) / tt; }
+__device__ __forceinline__ int paged_row_tiles(const PagedSeg &s, const PagedLine &l) {
+    return (s.qn + (1 << l.tt_shift) - 1) >> l.tt_shift;
+}
 
 // Tokens the last query of row tile m sees.
-__device__ __forceinline__ int paged_visible(const PagedSeg &s, int tt, int m) {
+__device__ __forceinline__ int paged_visible(const PagedSeg &s, const PagedLine &l, int m) {
     if (!s.own) return s.len;
-    const int last = min(s.qn, (m + 1) * tt) - 1;
+    const int last = min(s.qn, (m + 1) << l.tt_shift) - 1;
     return clampi(s.len - (s.qn - 1 - last), 0, s.len);
 }
 __device__ __forceinline__ int paged_steps(const PagedSeg &s, const PagedLine &l, int m) {
-    return (paged_visible(s, l.tt, m) + l.tile - 1) / l.tile;
+    return (paged_visible(s, l, m) + (1 << l.tile_shift) - 1) >> l.tile_shift;
 }
 // Steps of all row tiles before m, for one head.
 __device__ __forceinline__ int paged_steps_before(const PagedSeg &s, const PagedLine &l, int m) {
     if (!s.own) return m * paged_steps(s, l, 0);
     int w = 0;
+#pragma unroll 1
     for (int i = 0; i < m; ++i) w += paged_steps(s, l, i);
     return w;
 }
 
-// One warp's walk over the run of this CTA.  All lanes hold the same values.  The host has checked
+// One warp's walk over the run of this CTA.  A kernel calls start() and next() at one place each: a
+// launch begins with cold instruction caches and fetches its code line by line, so its size is time.  All lanes hold the same values.  The host has checked
 // that a whole line's steps and units fit 31 bits; a segment outside its range empties the line.
 struct PagedWalk {
     int w, w1;   // next step, end of the run
@@ -162,71 +173,79 @@ struct PagedWalk {
     __device__ __forceinline__ void load(const PagedArgs &a, const PagedLine &l) {
         bool bad = false;
         s = paged_segment(a, l, seg, bad);
-        nt = paged_row_tiles(s, l.tt);
+        nt = paged_row_tiles(s, l);
         per_head = paged_steps_before(s, l, nt);
     }
 
     // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also
-    // writes the line's record for the merge and reports bad segments.
-    __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c) {
+    // writes the line's record for the merge and reports bad segments, unless `dry`.  Two passes of
+    // the same loop: for the whole line's steps, and then for the place.
+    __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c, bool dry) {
         const int lane = threadIdx.x & 31;
         n = paged_segments(a, l);
-        int total = 0;
+        seg = n;
+        w = w1 = 0;
         bool bad = false;
 #pragma unroll 1
-        for (int i = lane; i < n; i += 32) {
-            const PagedSeg g = paged_segment(a, l, i, bad);
-            total += paged_steps_before(g, l, paged_row_tiles(g, l.tt)) * a.hkv;
-        }
-        total = __reduce_add_sync(0xFFFFFFFFu, total);
-        bad = __any_sync(0xFFFFFFFFu, bad);
-        if (bad) total = 0;
-        const int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
-        w = min((long long)total, (long long)c * per);
-        w1 = min(total, w + per);
-        seg = n;
-        if (c == 0 && lane == 0) {
-            l.rec[0] = make_int2(per, 0);
-            if (bad) raise_error(a.err, ERR_PAGE);
-        }
-        if (bad || (c != 0 && w >= w1)) {
-            w = w1;
-            return;
-        }
-        int wx = 0, ux = 0;
+        for (int pass = 0; pass < 2; ++pass) {
+            int wx = 0, ux = 0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane;
-            int mw = 0, mu = 0;
-            if (i < n) {
-                const PagedSeg g = paged_segment(a, l, i, bad);
-                const int t = paged_row_tiles(g, l.tt);
-                mw = paged_steps_before(g, l, t) * a.hkv;
-                mu = t * a.hkv;
-            }
-            int sw = mw, su = mu;  // inclusive sums over the lanes
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int pw = __shfl_up_sync(0xFFFFFFFFu, sw, o), pu = __shfl_up_sync(0xFFFFFFFFu, su, o);
-                if (lane >= o) {
-                    sw += pw;
-                    su += pu;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                PagedSeg g = {};
+                int gt = 0, gh = 0;  // row tiles, steps of one head
+                if (i0 + lane < n) {
+                    g = paged_segment(a, l, i0 + lane, bad);
+                    gt = paged_row_tiles(g, l);
+                    gh = paged_steps_before(g, l, gt);
                 }
+                const int mw = gh * a.hkv, mu = gt * a.hkv;
+                if (pass == 0) {
+                    wx += __reduce_add_sync(0xFFFFFFFFu, mw);
+                    continue;
+                }
+                int sw = mw, su = mu;  // inclusive sums over the lanes
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int pw = __shfl_up_sync(0xFFFFFFFFu, sw, o), pu = __shfl_up_sync(0xFFFFFFFFu, su, o);
+                    if (lane >= o) {
+                        sw += pw;
+                        su += pu;
+                    }
+                }
+                const int ew = wx + sw - mw, eu = ux + su - mu;
+                if (c == 0 && !dry && i0 + lane < n) l.rec[1 + i0 + lane] = make_int2(ew, eu);
+                const unsigned hit = __ballot_sync(0xFFFFFFFFu, w < w1 && w >= ew && w < ew + mw);
+                if (hit) {  // the run begins in this lane's segment
+                    const int at = __ffs(hit) - 1;
+                    seg = i0 + at;
+                    Wx = __shfl_sync(0xFFFFFFFFu, ew, at);
+                    Ux = __shfl_sync(0xFFFFFFFFu, eu, at);
+                    s.q0 = __shfl_sync(0xFFFFFFFFu, g.q0, at);
+                    s.qn = __shfl_sync(0xFFFFFFFFu, g.qn, at);
+                    s.len = __shfl_sync(0xFFFFFFFFu, g.len, at);
+                    s.row = __shfl_sync(0xFFFFFFFFu, g.row, at);
+                    s.own = __shfl_sync(0xFFFFFFFFu, (int)g.own, at) != 0;
+                    nt = __shfl_sync(0xFFFFFFFFu, gt, at);
+                    per_head = __shfl_sync(0xFFFFFFFFu, gh, at);
+                    if (c != 0) return;
+                }
+                wx += __shfl_sync(0xFFFFFFFFu, sw, 31);
+                ux += __shfl_sync(0xFFFFFFFFu, su, 31);
             }
-            const int ew = wx + sw - mw, eu = ux + su - mu;
-            if (c == 0 && i < n) l.rec[1 + i] = make_int2(ew, eu);
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, w < w1 && w >= ew && w < ew + mw);
-            if (hit && seg == n) {
-                const int at = __ffs(hit) - 1;
-                seg = i0 + at;
-                Wx = __shfl_sync(0xFFFFFFFFu, ew, at);
-                Ux = __shfl_sync(0xFFFFFFFFu, eu, at);
-                if (c != 0) break;
+            if (pass == 0) {
+                bad = __any_sync(0xFFFFFFFFu, bad);
+                const int per = bad ? 0 : (int)max(1u, ((unsigned)wx + l.ctas - 1) / (unsigned)l.ctas);
+                if (c == 0 && lane == 0 && !dry) {
+                    l.rec[0] = make_int2(per, 0);
+                    if (bad) raise_error(a.err, ERR_PAGE);
+                }
+                if (!bad) {
+                    w = (int)min((long long)wx, (long long)c * per);
+                    w1 = min(wx, w + per);
+                }
+                if (bad || (w >= w1 && c != 0)) return;
             }
-            wx += __shfl_sync(0xFFFFFFFFu, sw, 31);
-            ux += __shfl_sync(0xFFFFFFFFu, su, 31);
         }
-        if (seg < n) load(a, l); else w = w1;
     }
 
     // The next piece; false at the end of the run.
@@ -247,6 +266,7 @@ struct PagedWalk {
             m = (unsigned)r / (unsigned)steps;
             r -= m * steps;
         } else {
+#pragma unroll 1
             while (r >= steps) {
                 r -= steps;
                 if (++m >= nt) return false;  // lengths changed under the kernel
@@ -262,7 +282,9 @@ struct PagedWalk {
 };
 
 // 16-bit types of the pages.
+// SHIFT: weights are 2^(l - m + SHIFT), up to 2^8 in fp16, away from its subnormals.
 struct PgBf16 {
+    static constexpr float SHIFT = 0.0f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t y;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
@@ -277,6 +299,7 @@ struct PgBf16 {
     }
 };
 struct PgF16 {
+    static constexpr float SHIFT = 8.0f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t y;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
@@ -295,6 +318,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Wait for phase `parity` of the barrier; false when *abort is set or the time is up.  The clock and
+// the flag are looked at between runs of polls only: with each poll they add 300 cycles to a wake-up.
+__device__ __forceinline__ bool paged_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    unsigned long long t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity & 1u)) return true;
+        const unsigned long long t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (*abort || t - t0 > TMA_WAIT_NS) return false;
+    }
 }
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {

@@ -368,9 +368,9 @@ bool valid_pages(const verkv_pages *p, const verkv_shape &sh) {
     return valid_dtype(p->dtype) && (t == 16 || t == 32 || t == 64 || t == 128 || t == 256) && p->num_pages >= 1 && p->kv &&
            !bad16(p->kv) && (int64_t)p->num_pages * sh.kv_heads * t < (1LL << 31);
 }
-int page_shift(int page_tokens) {
+int log2_of(int power_of_two) {
     int s = 0;
-    while ((1 << s) < page_tokens) ++s;
+    while ((1 << s) < power_of_two) ++s;
     return s;
 }
 bool valid_rope(const verkv_rope *r, int d) {
@@ -431,17 +431,15 @@ constexpr int PAGED_MAX_SEGMENTS = 65536;  // sequences or prefixes of a call
 int64_t paged_rows(int64_t q_tokens, int64_t segments, int G) { return (q_tokens + segments - 1) / segments * G; }
 
 // A level whose segments have more rows than this goes through k_paged_wide, else k_paged.
-constexpr int PAGED_WIDE_ROWS = 32;
-
-// Rows of a row tile.
-int paged_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= PAGED_WIDE_ROWS ? 32 : rows <= 128 ? 128 : 256; }
+constexpr int PAGED_WIDE_ROWS = PAGED_ROWS;
 
 // Upper bound of the partial rows of any call for up to these sizes.  Of one level: its queries'
-// rows q G, at most one ragged row tile a segment, and one slot a CTA.  A level in tiles of 128 or
-// 256 rows has more than 32 rows a segment on average, so fewer than q G / (33 - G) segments, whose
-// ragged tiles add at most 256 / 25 q G.
+// rows q G, at most one ragged row tile a segment, and one slot a CTA.  A level in tiles of 128 rows
+// has more than 16 rows a segment on average, one in tiles of 256 more than 128: its ragged tiles add
+// at most 128 / 16 q G.
 int64_t paged_rows_bound(int64_t hkv, int64_t G, int64_t seqs, int64_t groups, int64_t q_tokens) {
-    return hkv * (2 * 12 * q_tokens * G + 32 * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * 32 + (int64_t)PAGED_WIDE_CTAS * 256;
+    return hkv * (2 * 9 * q_tokens * G + PAGED_ROWS * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * PAGED_ROWS +
+           (int64_t)PAGED_WIDE_CTAS * 256;
 }
 bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_shape &sh) {
     return seqs >= 0 && groups >= 0 && q_tokens >= 0 && seqs <= PAGED_MAX_SEGMENTS && groups <= PAGED_MAX_SEGMENTS &&
@@ -458,16 +456,16 @@ size_t paged_workspace(const verkv_shape &sh, int64_t seqs, int64_t groups, int6
 bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows_tile, int ctas_max, unsigned char *ws,
                 size_t &off) {
     const int64_t hkv = a.hkv;
-    l.tt = rows_tile / a.G;
+    l.tt_shift = log2_of(rows_tile) - a.g_shift;
     int64_t units = 0, steps = 0, segs = 0;
     auto level = [&](const PagedLevel &lv) {
-        const int64_t tiles = a.q_tokens / l.tt + lv.rows;
+        const int64_t tiles = (a.q_tokens >> l.tt_shift) + lv.rows;
         units += tiles * hkv;
-        steps += tiles * hkv * ((lv.max_length + l.tile - 1) / l.tile);
+        steps += tiles * hkv * ((lv.max_length + (1 << l.tile_shift) - 1) >> l.tile_shift);
         segs += lv.rows;
     };
-    if (l.with_prefix) level(a.prefix);
-    if (l.with_own) level(a.own);
+    for (int x = 0; x < 2; ++x)
+        if (l.with[x]) level(a.level[x]);
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
     if (steps >= (1LL << 31) || units + l.ctas >= (1LL << 31)) return false;
     l.slots = (int)(units + l.ctas);
@@ -1109,7 +1107,7 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
     a.hv = ctx->sh.kv_heads;
     a.pages = (uint16_t *)pages->kv;
     a.num_pages = pages->num_pages;
-    a.page_shift = page_shift(pages->page_tokens);
+    a.page_shift = log2_of(pages->page_tokens);
     a.seq = seq;
     a.index = index;
     a.table = span->table;
@@ -1175,13 +1173,13 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         if (s) l = {s->table, s->length, s->rows, s->stride, s->max_length};
         return l;
     };
-    a.prefix = level(prefix && prefix->max_length > 0 ? prefix : nullptr);
-    a.own = level(own && own->max_length > 0 ? own : nullptr);
+    a.level[0] = level(prefix && prefix->max_length > 0 ? prefix : nullptr);
+    a.level[1] = level(own && own->max_length > 0 ? own : nullptr);
     a.seqs = seqs;
     a.q_tokens = q_tokens;
     a.hkv = sh.kv_heads;
-    a.G = sh.q_per_kv;
-    a.page_shift = page_shift(pages->page_tokens);
+    a.g_shift = log2_of(sh.q_per_kv);
+    a.page_shift = log2_of(pages->page_tokens);
     a.num_pages = pages->num_pages;
     a.scale_log2 = (float)((scale == 0.0f ? 1.0 / sqrt((double)sh.head_dim) : (double)scale) * 1.4426950408889634);
     a.err = ctx->err;
@@ -1190,26 +1188,27 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
     a.o = (uint16_t *)o_out;
     a.lse = lse_out;
 
-    PagedLine lines[PAGED_LINES] = {};
+    PagedLines both{};
+    PagedLine *lines = both.l;
     size_t off = 0;
-    if (a.prefix.rows || a.own.rows) {
+    if (a.level[0].rows || a.level[1].rows) {
         // Each level by the rows of its segments; the two lines' launches need not wait for one another.
-        const int64_t rows_prefix = a.prefix.rows ? paged_rows(q_tokens, a.prefix.rows, a.G) : 0;
-        const int64_t rows_own = a.own.rows ? paged_rows(q_tokens, a.own.rows, a.G) : 0;
-        int64_t rows[PAGED_LINES] = {0, 0};
-        for (int w = 0; w < PAGED_LINES; ++w) {
-            lines[w].with_prefix = rows_prefix > 0 && (rows_prefix > PAGED_WIDE_ROWS) == (w == 1);
-            lines[w].with_own = rows_own > 0 && (rows_own > PAGED_WIDE_ROWS) == (w == 1);
-            if (lines[w].with_prefix) rows[w] = rows_prefix;
-            if (lines[w].with_own) rows[w] = std::max(rows[w], rows_own);
-        }
-        lines[0].tile = PAGED_TILE;
-        lines[1].tile = PAGED_WIDE_TILE;
+        const int64_t rows_prefix = a.level[0].rows ? paged_rows(q_tokens, a.level[0].rows, sh.q_per_kv) : 0;
+        const int64_t rows_own = a.level[1].rows ? paged_rows(q_tokens, a.level[1].rows, sh.q_per_kv) : 0;
+        const auto wide = [](int64_t rows) { return rows > PAGED_WIDE_ROWS; };
+        lines[0].with[0] = rows_prefix > 0 && !wide(rows_prefix);
+        lines[0].with[1] = rows_own > 0 && !wide(rows_own);
+        lines[1].with[0] = wide(rows_prefix);
+        lines[1].with[1] = wide(rows_own);
+        const bool few = lines[0].with[0] || lines[0].with[1], many = lines[1].with[0] || lines[1].with[1];
+        // Tiles of 256 rows where every level has that many: K and V are read half as often.
+        const bool tall = (!lines[1].with[0] || rows_prefix > 128) && (!lines[1].with[1] || rows_own > 128);
+        lines[0].tile_shift = log2_of(PAGED_TILE);
+        lines[1].tile_shift = log2_of(PAGED_WIDE_TILE);
         lines[1].grouped = 1;
-        const int t0 = paged_tile_rows(rows[0]), t1 = paged_tile_rows(rows[1]);
         bool ok = true;
-        if (rows[0]) ok &= paged_line(ctx, a, lines[0], t0, std::min(ctx->sms * (t0 == 16 ? 2 : 1), PAGED_MAX_CTAS), (unsigned char *)workspace, off);
-        if (rows[1]) ok &= paged_line(ctx, a, lines[1], t1, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
+        if (few) ok &= paged_line(ctx, a, lines[0], PAGED_ROWS, std::min(ctx->sms * 2, PAGED_MAX_CTAS), (unsigned char *)workspace, off);
+        if (many) ok &= paged_line(ctx, a, lines[1], tall ? 256 : 128, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
         if (!ok) return fail(ctx, VERKV_EINVAL, "paged_attend: more than 2^31 steps of work in one call");
         if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
         CUtensorMap map;
@@ -1217,18 +1216,18 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
             return paged_tensor_map(&map, pages->kv, pages->dtype, (long long)pages->num_pages * a.hkv * pages->page_tokens,
                                     sh.head_dim, std::min(pages->page_tokens, tile));
         };
-        if (rows[0]) {
+        if (few) {
             VERKV_CUDA(make_map(PAGED_TILE), "tensor map of the pages");
             VERKV_CUDA(tracked(ctx, VERKV_K_PAGED, ctx->main, [&] { return launch_paged(a, lines[0], map, pages->dtype, sh.head_dim, ctx->main); }), "k_paged");
         }
-        if (rows[1]) {
+        if (many) {
             VERKV_CUDA(make_map(PAGED_WIDE_TILE), "tensor map of the pages");
             VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_WIDE, ctx->main, [&] {
-                           return launch_paged_wide(a, lines[1], map, rows[0] == 0 || ctx->prof_on, pages->dtype, sh.head_dim, ctx->main);
+                           return launch_paged_wide(a, lines[1], map, !few || ctx->prof_on, pages->dtype, sh.head_dim, ctx->main);
                        }), "k_paged_wide");
         }
     }
-    VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_MERGE, ctx->main, [&] { return launch_paged_merge(a, lines, pages->dtype, sh.head_dim, ctx->main); }), "k_paged_merge");
+    VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_MERGE, ctx->main, [&] { return launch_paged_merge(a, both, pages->dtype, sh.head_dim, ctx->main); }), "k_paged_merge");
     return VERKV_OK;
 } catch (...) {
     return VERKV_ECUDA;
