@@ -341,7 +341,7 @@ typedef struct {
  * head_dim; 0: none).  Channel pair j = 0 .. rotary_dim / 2 - 1 is (j, j + rotary_dim / 2), or
  * (2 j, 2 j + 1) when interleaved is not 0; at position p it turns by p * inv_freq[j]:
  * (a, b) -> (a cos - b sin, b cos + a sin).
- *   turns  device uint64 [rotary_dim / 2], 8-byte aligned: from verkv_rope_turns */
+ *   turns  device uint64 [rotary_dim / 2], 16-byte aligned: from verkv_rope_turns */
 typedef struct {
     int32_t rotary_dim;
     int32_t interleaved;

@@ -11,10 +11,13 @@
 // far below half a step of the 16-bit result.
 //
 // Bound: the rows' bytes (2 d each way per head) for prompts, one launch for a decode step.  A row
-// takes d / 8 lanes of 16 bytes, so a warp holds 2 (d = 128) or 4 rows at once; the square sums
-// and the partner channel of a rotation (rotary_dim / 2 channels away: whole lanes) move by
-// shuffles, and nothing goes through shared memory.  A warp takes PASSES times that many rows of
-// one token, loads them all before it computes, and makes the token's sines once for them.
+// takes d / 8 lanes, each holding two groups of four channels: rotated in halves, a channel and its
+// partner rotary_dim / 2 away are in the same lane, rotated in pairs, neighbours are, so that a
+// rotation moves nothing between lanes and a lane makes four sines.  Only the square sums go by
+// shuffle.  A warp takes PASSES rounds of 2 (d = 128) or 4 rows of one token, all queries, keys or
+// values; it loads them all, makes the token's sines once, folds the norm's weights into them --
+//   out_a = s (x_a (w_a cos) - x_b (w_b sin)),  out_b = s (x_b (w_b cos) + x_a (w_a sin)),  s = 1 / rms
+// -- and then spends three packed operations a channel pair.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -46,14 +49,55 @@ struct F16 {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 p = T::up(w[i]);
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
+// Two floats in one register pair: the packed arithmetic of this architecture.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+    f32x2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ float2 split(f32x2 v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// A lane's eight channels as x[0..1] and their partners y[0..1], pairs of floats: in halves the
+// channels of `a` and `b`; in pairs (IL) the even and the odd ones of both.
+template <typename T, bool IL>
+__device__ __forceinline__ void unpack(const uint2 &a, const uint2 &b, f32x2 (&x)[2], f32x2 (&y)[2]) {
+    const float2 a0 = T::up(a.x), a1 = T::up(a.y), b0 = T::up(b.x), b1 = T::up(b.y);
+    if (IL) {
+        x[0] = pair(a0.x, a1.x);
+        x[1] = pair(b0.x, b1.x);
+        y[0] = pair(a0.y, a1.y);
+        y[1] = pair(b0.y, b1.y);
+    } else {
+        x[0] = pair(a0.x, a0.y);
+        x[1] = pair(a1.x, a1.y);
+        y[0] = pair(b0.x, b0.y);
+        y[1] = pair(b1.x, b1.y);
+    }
+}
+template <typename T, bool IL>
+__device__ __forceinline__ void repack(const f32x2 (&x)[2], const f32x2 (&y)[2], uint2 &a, uint2 &b) {
+    const float2 x0 = split(x[0]), x1 = split(x[1]), y0 = split(y[0]), y1 = split(y[1]);
+    if (IL) {
+        a = make_uint2(T::down(x0.x, y0.x), T::down(x0.y, y0.y));
+        b = make_uint2(T::down(x1.x, y1.x), T::down(x1.y, y1.y));
+    } else {
+        a = make_uint2(T::down(x0.x, x0.y), T::down(x1.x, x1.y));
+        b = make_uint2(T::down(y0.x, y0.y), T::down(y1.x, y1.y));
     }
 }
 
@@ -67,121 +111,135 @@ __device__ __forceinline__ void turn_sincos(int32_t pos, uint64_t turns, float &
     c = __cosf(x);
 }
 
-template <typename T, int D, int PASSES>
-__global__ void __launch_bounds__(HD_NT) k_heads(const HeadsArgs a) {
+template <typename T, int D, int PASSES, bool IL>
+__global__ void __launch_bounds__(HD_NT) k_heads(const __grid_constant__ HeadsArgs a) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows a warp holds at once
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, li = lane % LPR, ch = li * 8;
-    const long long item = (long long)blockIdx.x * (HD_NT / 32) + (threadIdx.x >> 5);
-    const int t = (int)(item / a.chunks);
+    const int lane = threadIdx.x & 31, li = lane % LPR;
+    const int item = blockIdx.x * (HD_NT / 32) + (threadIdx.x >> 5);
+    const int t = (unsigned)item / (unsigned)a.chunks;
     if (t >= a.tokens) return;
-    const int row0 = (int)(item - (long long)t * a.chunks) * (PASSES * RPW) + lane / LPR;
-    const int rows = a.hq + a.hk + a.hv;
+    int c = item - t * a.chunks;
+    const int kind = c < a.chunks_q ? 0 : c < a.chunks_q + a.chunks_k ? 1 : 2;  // queries, keys, values
+    c -= kind == 0 ? 0 : kind == 1 ? a.chunks_q : a.chunks_q + a.chunks_k;
+    const int rows = kind == 0 ? a.hq : kind == 1 ? a.hk : a.hv;
+    const long long hs = kind == 0 ? a.q_hs : kind == 1 ? a.k_hs : a.v_hs;
+    const int row0 = c * (PASSES * RPW) + lane / LPR;
 
-    uint4 x[PASSES];
+    // This lane's two groups of channels, at ca and cb.  In halves: partners while the lane's share of
+    // the rotated part lasts, then channels that are not rotated; in pairs: neighbours.
+    const bool turned = li < (a.rd >> 3);
+    int ca = li * 8, cb = ca + 4;
+    if (!IL && turned) {
+        ca = li * 4;
+        cb = ca + (a.rd >> 1);
+    }
+
+    const uint16_t *src = (kind == 0 ? a.q + t * a.q_ts : kind == 1 ? a.k + t * a.k_ts : a.v + t * a.v_ts) + row0 * hs;
+    uint2 xa[PASSES], xb[PASSES];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-        const int r = row0 + p * RPW;
-        x[p] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-            const uint16_t *src =
-                r < a.hq ? a.q + t * a.q_ts + r * a.q_hs
-                : r < a.hq + a.hk ? a.k + t * a.k_ts + (r - a.hq) * a.k_hs
-                                  : a.v + t * a.v_ts + (r - a.hq - a.hk) * a.v_hs;
-            x[p] = *reinterpret_cast<const uint4 *>(src + ch);
+        xa[p] = xb[p] = make_uint2(0u, 0u);
+        if (row0 + p * RPW < rows) {
+            // many rows pass once: not worth a place in the cache (a 32K prompt's append 57 -> 47 us)
+            xa[p] = PASSES > 1 ? __ldcs(reinterpret_cast<const uint2 *>(src + ca)) : *reinterpret_cast<const uint2 *>(src + ca);
+            xb[p] = PASSES > 1 ? __ldcs(reinterpret_cast<const uint2 *>(src + cb)) : *reinterpret_cast<const uint2 *>(src + cb);
         }
+        src += RPW * hs;
     }
 
-    // The rotation of this lane's channels.  Half style: pair of channel c is c mod (rd / 2), and
-    // its partner sits rd / 16 lanes away; interleaved: pairs lie within the lane.
-    const int half = a.rd >> 1;
-    const bool turned = ch < a.rd;
-    const bool second = !a.interleaved && ch >= half;
-    float sn[8], cs[8];
-    if (a.rd > 0) {
-        const int32_t pos = a.positions[t];
-        const int n = a.interleaved ? 4 : 8;
-        const int j0 = a.interleaved ? ch >> 1 : second ? ch - half : ch;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sn[i] = 0.0f;
-            cs[i] = 1.0f;
-            if (i < n && turned) turn_sincos(pos, a.turns[j0 + i], sn[i], cs[i]);
-        }
-    }
-    uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
-    if (a.wq) wq = *reinterpret_cast<const uint4 *>(a.wq + ch);
-    if (a.wk) wk = *reinterpret_cast<const uint4 *>(a.wk + ch);
-
-    // Where this token's keys and values go in the pages: element of its slot for head 0, or -1.
-    long long place = -1;
-    if (a.pages && row0 + (PASSES - 1) * RPW >= a.hq) {
+    // Where the rows go.
+    uint16_t *dst;
+    long long ds;
+    if (kind == 0) {
+        dst = a.q_out + t * a.qo_ts;
+        ds = a.qo_hs;
+    } else if (!a.pages) {
+        dst = a.k_out + t * a.ko_ts;
+        ds = a.ko_hs;
+    } else {
         const int s = a.seq[t];
-        if (s != -1) {
-            const int i = a.index[t], pg = i >> a.page_shift;
-            int page = -1;
-            if (s >= 0 && s < a.table_rows && i >= 0 && pg < a.table_stride)
-                page = a.table[(long long)s * a.table_stride + pg];
-            if (page >= 0 && page < a.num_pages)
-                place = (((long long)page * a.hk << a.page_shift) + (i & ((1 << a.page_shift) - 1))) * (2 * D);
-            else if (lane == 0)
-                raise_error(a.err, ERR_PAGE);
+        if (s == -1) return;
+        const int i = a.index[t], pg = i >> a.page_shift;
+        int page = -1;
+        if (s >= 0 && s < a.table_rows && i >= 0 && pg < a.table_stride)
+            page = a.table[(long long)s * a.table_stride + pg];
+        if (page < 0 || page >= a.num_pages) {
+            if (lane == 0) raise_error(a.err, ERR_PAGE);
+            return;
+        }
+        dst = a.pages + (((long long)page * a.hk << a.page_shift) + (i & ((1 << a.page_shift) - 1))) * (2 * D) + (kind == 2 ? D : 0);
+        ds = (long long)(2 * D) << a.page_shift;
+    }
+    dst += row0 * ds;
+
+    const uint16_t *w = kind == 0 ? a.wq : a.wk;
+    const bool norm = kind != 2 && w;
+    if (norm || (kind != 2 && a.rd > 0)) {
+        // Coefficients of x and y in the two results.
+        f32x2 xc[2], ys[2], yc[2], xs[2], wx[2], wy[2];
+        wx[0] = wx[1] = wy[0] = wy[1] = pair(1.0f, 1.0f);
+        if (norm) unpack<T, IL>(*reinterpret_cast<const uint2 *>(w + ca), *reinterpret_cast<const uint2 *>(w + cb), wx, wy);
+        float sn[4] = {0.0f, 0.0f, 0.0f, 0.0f}, cs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        if (turned) {  // pairs li * 4 .. + 3 in either order
+            const int32_t pos = a.positions[t];
+            const ulonglong2 *tp = reinterpret_cast<const ulonglong2 *>(a.turns + li * 4);
+            const ulonglong2 t0 = tp[0], t1 = tp[1];
+            turn_sincos(pos, t0.x, sn[0], cs[0]);
+            turn_sincos(pos, t0.y, sn[1], cs[1]);
+            turn_sincos(pos, t1.x, sn[2], cs[2]);
+            turn_sincos(pos, t1.y, sn[3], cs[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const f32x2 co = pair(cs[2 * i], cs[2 * i + 1]), si = pair(sn[2 * i], sn[2 * i + 1]);
+            xc[i] = mul2(wx[i], co);
+            yc[i] = mul2(wy[i], co);
+            xs[i] = mul2(wx[i], si);
+            ys[i] = mul2(wy[i], pair(-sn[2 * i], -sn[2 * i + 1]));
+        }
+        const bool whole = a.rd == D;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            f32x2 x[2], y[2], u[2], v[2];
+            unpack<T, IL>(xa[p], xb[p], x, y);
+            f32x2 inv = pair(1.0f, 1.0f);
+            if (norm) {
+                const float2 ss = split(fma2(x[0], x[0], fma2(x[1], x[1], fma2(y[0], y[0], mul2(y[1], y[1])))));
+                float sum = ss.x + ss.y;
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                const float r = rsqrtf(sum * (1.0f / D) + a.eps);
+                inv = pair(r, r);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                u[i] = mul2(x[i], xc[i]);
+                v[i] = mul2(y[i], yc[i]);
+                // a channel that is not rotated stays apart from the other, which may be no number
+                if (whole || turned) {
+                    u[i] = fma2(y[i], ys[i], u[i]);
+                    v[i] = fma2(x[i], xs[i], v[i]);
+                }
+                u[i] = mul2(u[i], inv);
+                v[i] = mul2(v[i], inv);
+            }
+            repack<T, IL>(u, v, xa[p], xb[p]);
         }
     }
-
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-        const int r = row0 + p * RPW;
-        const bool is_q = r < a.hq, is_v = r >= a.hq + a.hk;
-        uint4 y = x[p];
-        float f[8];
-        unpack<T>(x[p], f);
-        if (a.wq || a.wk) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-            const uint4 w = is_q ? wq : wk;
-            if (is_q ? a.wq != nullptr : a.wk != nullptr) {
-                const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-                float g[8];
-                unpack<T>(w, g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] *= inv * g[i];
-            }
-        }
-        if (a.rd > 0) {
-            if (a.interleaved) {
-                if (turned) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = f[2 * i], v = f[2 * i + 1];
-                        f[2 * i] = u * cs[i] - v * sn[i];
-                        f[2 * i + 1] = v * cs[i] + u * sn[i];
-                    }
-                }
+        if (row0 + p * RPW < rows) {
+            if (PASSES > 1) {
+                __stcs(reinterpret_cast<uint2 *>(dst + ca), xa[p]);
+                __stcs(reinterpret_cast<uint2 *>(dst + cb), xb[p]);
             } else {
-                const int partner = !turned ? lane : second ? lane - half / 8 : lane + half / 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float o = __shfl_sync(0xFFFFFFFFu, f[i], partner);
-                    if (turned) f[i] = second ? f[i] * cs[i] + o * sn[i] : f[i] * cs[i] - o * sn[i];
-                }
+                *reinterpret_cast<uint2 *>(dst + ca) = xa[p];
+                *reinterpret_cast<uint2 *>(dst + cb) = xb[p];
             }
         }
-        if (!is_v) y = make_uint4(T::down(f[0], f[1]), T::down(f[2], f[3]), T::down(f[4], f[5]), T::down(f[6], f[7]));
-        if (r >= rows) continue;  // no shuffle below
-        uint16_t *dst = nullptr;
-        if (is_q)
-            dst = a.q_out + t * a.qo_ts + r * a.qo_hs;
-        else if (!a.pages)
-            dst = a.k_out + t * a.ko_ts + (r - a.hq) * a.ko_hs;
-        else if (place >= 0)
-            dst = a.pages + place + ((long long)(is_v ? r - a.hq - a.hk : r - a.hq) << a.page_shift) * (2 * D) +
-                  (is_v ? D : 0);
-        if (dst) *reinterpret_cast<uint4 *>(dst + ch) = y;
+        dst += RPW * ds;
     }
 }
 
@@ -189,14 +247,23 @@ __global__ void __launch_bounds__(HD_NT) k_heads(const HeadsArgs a) {
 
 cudaError_t launch_heads(const HeadsArgs &args, int dtype, int d, cudaStream_t s) {
     HeadsArgs a = args;
-    const int rows = a.hq + a.hk + a.hv, rpw = 256 / d;
+    const int rpw = 256 / d;
+    // One round a warp while that fills no more than half the warps the GPU holds (below about 250 tokens
+    // of 40 heads; 64 tokens 2.2 against 2.6 us, 1024 tokens 7.2 against 5.3), else four.
     int passes = 4;
-    if ((long long)a.tokens * rows < 152LL * 64 * rpw) passes = 1;
-    a.chunks = (rows + passes * rpw - 1) / (passes * rpw);
-    const long long blocks = ((long long)a.tokens * a.chunks + HD_NT / 32 - 1) / (HD_NT / 32);
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-#define VERKV_HEADS(TT, DT, DD, PP) \
-    if (dtype == DT && d == DD && passes == PP) return launch_pdl(k_heads<TT, DD, PP>, dim3((unsigned)blocks), dim3(HD_NT), 0, s, a);
+    if ((long long)a.tokens * (a.hq + a.hk + a.hv) < 152LL * 32 * rpw) passes = 1;
+    const auto chunks = [&](int rows) { return (rows + passes * rpw - 1) / (passes * rpw); };
+    a.chunks_q = chunks(a.hq);
+    a.chunks_k = chunks(a.hk);
+    a.chunks = a.chunks_q + a.chunks_k + chunks(a.hv);
+    const long long items = (long long)a.tokens * a.chunks, blocks = (items + HD_NT / 32 - 1) / (HD_NT / 32);
+    if (items + HD_NT / 32 > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const bool il = a.interleaved && a.rd > 0;
+#define VERKV_HEADS(TT, DT, DD, PP)                                                                                        \
+    if (dtype == DT && d == DD && passes == PP) {                                                                          \
+        if (il) return launch_pdl(k_heads<TT, DD, PP, true>, dim3((unsigned)blocks), dim3(HD_NT), 0, s, a);                \
+        return launch_pdl(k_heads<TT, DD, PP, false>, dim3((unsigned)blocks), dim3(HD_NT), 0, s, a);                       \
+    }
     VERKV_HEADS(Bf16, VERKV_BF16, 128, 1) VERKV_HEADS(Bf16, VERKV_BF16, 128, 4)
     VERKV_HEADS(Bf16, VERKV_BF16, 64, 1) VERKV_HEADS(Bf16, VERKV_BF16, 64, 4)
     VERKV_HEADS(F16, VERKV_F16, 128, 1) VERKV_HEADS(F16, VERKV_F16, 128, 4)

@@ -33,7 +33,7 @@ struct HeadsArgs {
     const int32_t *positions, *seq, *index, *table;
     uint32_t *err;
     int tokens, hq, hk, hv;  // heads of each token to do: queries, keys, values
-    int chunks;              // warps a token takes (set by the launcher)
+    int chunks, chunks_q, chunks_k;  // warps a token takes, of them for queries and keys (set by the launcher)
     int rd, interleaved;
     int table_rows, table_stride, num_pages, page_shift;
     float eps;

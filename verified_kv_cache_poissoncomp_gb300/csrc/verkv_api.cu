@@ -375,7 +375,7 @@ int log2_of(int power_of_two) {
 }
 bool valid_rope(const verkv_rope *r, int d) {
     return r->rotary_dim >= 0 && r->rotary_dim <= d && r->rotary_dim % 16 == 0 &&
-           (r->rotary_dim == 0 || (r->turns && ((uintptr_t)r->turns & 7u) == 0));
+           (r->rotary_dim == 0 || (r->turns && !bad16(r->turns)));
 }
 
 // What norm_rotate and append have in common; nullptr, or what is wrong.
@@ -412,7 +412,7 @@ const char *heads_args(const verkv_ctx *ctx, HeadsArgs &a, int32_t dtype, int32_
         a.eps = norm->eps;
     }
     if (rope) {
-        if (!valid_rope(rope, d)) return "rotary_dim must be a multiple of 16 up to head_dim, turns 8-byte aligned";
+        if (!valid_rope(rope, d)) return "rotary_dim must be a multiple of 16 up to head_dim, turns 16-byte aligned";
         a.rd = rope->rotary_dim;
         a.interleaved = rope->interleaved != 0;
         a.turns = rope->turns;
