@@ -327,7 +327,7 @@ def test_refusals():
             pytest.fail(f"call {i} was not refused")
         assert e.value.status == B.VERKV_EINVAL
     # the workspace
-    L, q = B.lib(), c.cache._rows(c.q, 4, "q")
+    L, q = B.lib(), c.cache._rows(c.q, 3, 4, "q")
     own = B.verkv_span(c.table.data_ptr(), 3, c.table.shape[1], c.lengths.data_ptr(), 100)
     need = B.verkv_paged_workspace_size(c.cache.shape, 3, 0, 3)
     ws, o = torch.empty(need + 256, dtype=torch.uint8, device="cuda"), torch.empty_like(c.q)

@@ -1065,6 +1065,7 @@ verkv_status verkv_norm_rotate(verkv_ctx *ctx, int32_t dtype, int32_t tokens, co
                                const verkv_rows *k_out, const verkv_head_norm *norm,
                                const verkv_rope *rope, const int32_t *positions) try {
     if (!ctx) return VERKV_EINVAL;
+    if (tokens == 0) return VERKV_OK;
     HeadsArgs a{};
     if (const char *why = heads_args(ctx, a, dtype, tokens, q, q_out, k, norm, rope, positions))
         return fail(ctx, VERKV_EINVAL, std::string("norm_rotate: ") + why);
@@ -1077,7 +1078,6 @@ verkv_status verkv_norm_rotate(verkv_ctx *ctx, int32_t dtype, int32_t tokens, co
         a.ko_ts = k_out->token_stride;
         a.ko_hs = k_out->head_stride;
     }
-    if (tokens == 0) return VERKV_OK;
     const DeviceRestore restore;
     VERKV_CUDA(cudaSetDevice(ctx->device), "cudaSetDevice");
     const NvtxRange nvtx("verkv_norm_rotate");
@@ -1093,6 +1093,7 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
                                 const verkv_rope *rope, const int32_t *positions,
                                 const int32_t *seq, const int32_t *index, const verkv_span *span) try {
     if (!ctx) return VERKV_EINVAL;
+    if (tokens == 0) return VERKV_OK;
     if (!pages || !k || !v || !seq || !index || !span || !span->table) return fail(ctx, VERKV_EINVAL, "paged_append: null pointer");
     if (!valid_pages(pages, ctx->sh)) return fail(ctx, VERKV_EINVAL, "paged_append: bad pool of pages");
     if (span->rows < 1 || span->stride < 1) return fail(ctx, VERKV_EINVAL, "paged_append: an empty table");
@@ -1113,7 +1114,6 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
     a.table = span->table;
     a.table_rows = span->rows;
     a.table_stride = span->stride;
-    if (tokens == 0) return VERKV_OK;
     const DeviceRestore restore;
     VERKV_CUDA(cudaSetDevice(ctx->device), "cudaSetDevice");
     const NvtxRange nvtx("verkv_paged_append");
@@ -1136,6 +1136,7 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
                                 void *workspace, size_t workspace_bytes) try {
     if (!ctx) return VERKV_EINVAL;
     const verkv_shape &sh = ctx->sh;
+    if (q_tokens == 0 && seqs >= 0) return VERKV_OK;
     if (!pages || !q || !o_out || !workspace) return fail(ctx, VERKV_EINVAL, "paged_attend: null pointer");
     if (!valid_pages(pages, sh)) return fail(ctx, VERKV_EINVAL, "paged_attend: bad pool of pages");
     const int groups = prefix ? prefix->rows : 0;
@@ -1157,7 +1158,6 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         return fail(ctx, VERKV_EINVAL, "paged_attend: prior_o and o_out need 16-byte, other arrays 4-byte alignment");
     if (((uintptr_t)workspace & 255u) || workspace_bytes < paged_workspace(sh, seqs, groups, q_tokens))
         return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small or not 256-byte aligned");
-    if (q_tokens == 0) return VERKV_OK;
     const DeviceRestore restore;
     VERKV_CUDA(cudaSetDevice(ctx->device), "cudaSetDevice");
     const NvtxRange nvtx("verkv_paged_attend");

@@ -8,11 +8,13 @@ work is libverkv's (verkv_norm_rotate, verkv_paged_append, verkv_paged_attend).
     q = cache.append(layer, k, v, seq, index, table, positions=pos, rope=rope, q=q, ...)
     o, lse = cache.attend(layer, q, table, lengths, max_length, prior=(eng.o, eng.lse))
 """
-import ctypes
-
 import torch
 
 from . import binding as B
+
+# The current stream's handle without a Stream object around it, where torch offers that.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 _DTYPES = {torch.bfloat16: B.VERKV_BF16, torch.float16: B.VERKV_F16}
 
@@ -71,53 +73,71 @@ class PagedKV:
             self.ctx = B.verkv_create(self.dev.index, self.stream.cuda_stream, self.shape,
                                       self._ctx_ws.data_ptr(), ws)
         self._raw_stream = self.stream.cuda_stream
-        # Workspaces of attend, largest last.  None is let go of: a captured graph may hold it.
+        self._index, self._lib = self.dev.index, B.lib()
+        # Workspaces of attend, largest last, and how many bytes each size of call needs.  None is let
+        # go of: a captured graph may hold it.
         self._spaces, self._needs = [], {}
+        self._space_at, self._space_bytes = None, 0
 
     # --------------------------------------------------------------------------------------------
+    # Checks and descriptors.  A decode step makes these calls once a layer, so they take the tensors'
+    # attributes once each and call the library directly.
     def _ready(self):
-        if torch.cuda.current_stream(self.dev).cuda_stream != self._raw_stream:
+        if _current_stream(self._index) != self._raw_stream:
             raise ValueError("another stream is current than the one this object was made on")
 
-    def _rows(self, t, heads, name):
+    def _fail(self, status):
+        raise B.VerkvError(status, B.verkv_last_error(self.ctx))
+
+    def _rows(self, t, tokens, heads, name):
         s = t.shape
-        if t.dtype != self.dtype or t.device != self.dev or len(s) != 3 or s[1] != heads or s[2] != self.d:
-            raise ValueError(f"{name}: a {self.dtype} tensor [tokens][{heads}][{self.d}] on {self.dev} is required")
-        st = t.stride()
-        if st[2] != 1 and s[0] > 0:
+        if t.dtype is not self.dtype or t.device != self.dev or len(s) != 3 or s[0] != tokens or s[1] != heads or s[2] != self.d:
+            raise ValueError(f"{name}: a {self.dtype} tensor [{tokens}][{heads}][{self.d}] on {self.dev} is required")
+        a, b, c = t.stride()
+        if c != 1 and tokens:
             raise ValueError(f"{name}: channels must be contiguous")
-        return B.verkv_rows(t.data_ptr(), st[0] if s[0] > 1 else 0, st[1] if heads > 1 else 0)
+        return B.verkv_rows(t.data_ptr(), a if tokens > 1 else 0, b if heads > 1 else 0)
+
+    def _out(self, out, tokens, heads, name):
+        """An output of the caller's, or a new one: the tensor and its descriptor."""
+        if out is not None:
+            return out, self._rows(out, tokens, heads, name)
+        d = self.d
+        out = torch.empty((tokens, heads, d), dtype=self.dtype, device=self.dev)
+        return out, B.verkv_rows(out.data_ptr(), heads * d, d)
 
     def _ints(self, t, shape, name):
-        if t.dtype != torch.int32 or t.device != self.dev or tuple(t.shape) != shape or not t.is_contiguous():
+        if t.dtype is not torch.int32 or t.device != self.dev or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: a contiguous int32 {list(shape)} tensor on {self.dev} is required")
         return t.data_ptr()
+
+    def _table(self, t, name):
+        s = t.shape
+        if len(s) != 2:
+            raise ValueError(f"{name}: an int32 tensor of page ids [rows][pages] is required")
+        return self._ints(t, s, name), s[0], s[1]
 
     def _weight(self, t, name):
         if t is None:
             return None
-        if t.dtype != self.dtype or t.device != self.dev or tuple(t.shape) != (self.d,) or not t.is_contiguous():
+        if t.dtype is not self.dtype or t.device != self.dev or t.shape != (self.d,) or not t.is_contiguous():
             raise ValueError(f"{name}: a contiguous {self.dtype} [{self.d}] tensor on {self.dev} is required")
         return t.data_ptr()
-
-    def _rope(self, rope):
-        if rope is None:
-            return None
-        if rope.dev != self.dev:
-            raise ValueError(f"rope: made for {rope.dev}, not {self.dev}")
-        return rope.desc
-
-    def _positions(self, positions, rope, tokens):
-        if positions is None:
-            if rope is not None:
-                raise ValueError("positions: needed for a rotation")
-            return None
-        return self._ints(positions, (tokens,), "positions")
 
     def _norm(self, q_weight, k_weight, eps):
         if q_weight is None and k_weight is None:
             return None
         return B.verkv_head_norm(self._weight(q_weight, "q_weight"), self._weight(k_weight, "k_weight"), eps)
+
+    def _turn(self, rope, positions, tokens):
+        """Descriptor of the rotation and address of the positions."""
+        if rope is None:
+            return None, None
+        if rope.dev != self.dev:
+            raise ValueError(f"rope: made for {rope.dev}, not {self.dev}")
+        if positions is None:
+            raise ValueError("positions: needed for a rotation")
+        return rope.desc, self._ints(positions, (tokens,), "positions")
 
     def _layer(self, layer):
         if self.kv is None:
@@ -135,30 +155,24 @@ class PagedKV:
         bytes.  An output may be the input itself; by default it is new.  A weight of None leaves
         those heads as long as they are.  Returns (q_out, k_out)."""
         self._ready()
-        some = q if q is not None else k
-        if some is None:
+        if q is None and k is None:
             raise ValueError("q or k is required")
-        tokens = some.shape[0]
-        desc = []
-        outs = []
-        for t, out, heads, name in ((q, q_out, self.hq, "q"), (k, k_out, self.h, "k")):
-            if t is None:
-                if out is not None:
-                    raise ValueError(f"{name}_out: given without {name}")
-                desc += [None, None]
-                outs.append(None)
-                continue
-            if out is None:
-                out = torch.empty((t.shape[0], heads, self.d), dtype=self.dtype, device=self.dev)
-            if t.shape[0] != tokens or out.shape[0] != tokens:
-                raise ValueError(f"{name}: {tokens} tokens are required")
-            desc += [self._rows(t, heads, name), self._rows(out, heads, name + "_out")]
-            outs.append(out)
-        pos = self._positions(positions, rope, tokens)
-        if tokens:
-            B.verkv_norm_rotate(self.ctx, self._code, tokens, *desc, self._norm(q_weight, k_weight, eps),
-                                self._rope(rope), pos)
-        return tuple(outs)
+        if (q is None and q_out is not None) or (k is None and k_out is not None):
+            raise ValueError("an output is given without its input")
+        tokens = (k if q is None else q).shape[0]
+        rq = ro = rk = rl = None
+        if q is not None:
+            rq = self._rows(q, tokens, self.hq, "q")
+            q_out, ro = self._out(q_out, tokens, self.hq, "q_out")
+        if k is not None:
+            rk = self._rows(k, tokens, self.h, "k")
+            k_out, rl = self._out(k_out, tokens, self.h, "k_out")
+        turn, pos = self._turn(rope, positions, tokens)
+        norm = self._norm(q_weight, k_weight, eps)
+        st = self._lib.verkv_norm_rotate(self.ctx, self._code, tokens, rq, ro, rk, rl, norm, turn, pos)
+        if st:
+            self._fail(st)
+        return q_out, k_out
 
     def append(self, layer, k, v, seq, index, table, positions=None, rope=None, k_weight=None,
                eps=1e-6, q=None, q_weight=None, q_out=None):
@@ -169,28 +183,21 @@ class PagedKV:
         positions: int32 [tokens]; table: int32 [sequences][pages].  Returns q_out (None without q)."""
         self._ready()
         tokens = k.shape[0]
-        rk, rv = self._rows(k, self.h, "k"), self._rows(v, self.h, "v")
+        rk, rv = self._rows(k, tokens, self.h, "k"), self._rows(v, tokens, self.h, "v")
         rq = ro = None
         if q is not None:
-            if q_out is None:
-                q_out = torch.empty((q.shape[0], self.hq, self.d), dtype=self.dtype, device=self.dev)
-            rq, ro = self._rows(q, self.hq, "q"), self._rows(q_out, self.hq, "q_out")
-            if q.shape[0] != tokens or q_out.shape[0] != tokens:
-                raise ValueError(f"q: {tokens} tokens are required")
+            rq = self._rows(q, tokens, self.hq, "q")
+            q_out, ro = self._out(q_out, tokens, self.hq, "q_out")
         elif q_out is not None:
             raise ValueError("q_out: given without q")
-        if v.shape[0] != tokens:
-            raise ValueError(f"v: {tokens} tokens are required")
-        if table.dim() != 2:
-            raise ValueError("table: int32 [sequences][pages] is required")
-        span = B.verkv_span(self._ints(table, tuple(table.shape), "table"), table.shape[0], table.shape[1], None, 0)
-        pos = self._positions(positions, rope, tokens)
+        at, rows, stride = self._table(table, "table")
+        turn, pos = self._turn(rope, positions, tokens)
+        norm = self._norm(q_weight if q is not None else None, k_weight, eps)
         ps, pi = self._ints(seq, (tokens,), "seq"), self._ints(index, (tokens,), "index")
-        pages = self._layer(layer)
-        if tokens:
-            B.verkv_paged_append(self.ctx, pages, tokens, rk, rv, rq, ro,
-                                 self._norm(q_weight if q is not None else None, k_weight, eps),
-                                 self._rope(rope), pos, ps, pi, span)
+        st = self._lib.verkv_paged_append(self.ctx, self._layer(layer), tokens, rk, rv, rq, ro, norm, turn, pos, ps, pi,
+                                          B.verkv_span(at, rows, stride, None, 0))
+        if st:
+            self._fail(st)
         return q_out
 
     def attend(self, layer, q, table, lengths, max_length, q_start=None, prefix_table=None,
@@ -209,59 +216,60 @@ class PagedKV:
 
         Returns (o [queries][heads][head_dim] of the pool's type, lse float32 [queries][heads])."""
         self._ready()
-        tokens = q.shape[0]
-        rq = self._rows(q, self.hq, "q")
-        own = prefix = None
+        tokens, hq, dev = q.shape[0], self.hq, self.dev
+        rq = self._rows(q, tokens, hq, "q")
+        own = prefix = ps = pg = po = pl = None
+        groups = 0
         if table is not None:
-            if table.dim() != 2:
-                raise ValueError("table: int32 [sequences][pages] is required")
-            n = table.shape[0]
+            at, n, stride = self._table(table, "table")
+            if n:
+                own = B.verkv_span(at, n, stride, self._ints(lengths, (n,), "lengths"), max_length)
         else:
             n = tokens if q_start is None else q_start.shape[0] - 1
-        if table is not None and n > 0:
-            own = B.verkv_span(self._ints(table, tuple(table.shape), "table"), n, table.shape[1],
-                               self._ints(lengths, (n,), "lengths"), max_length)
-        ps = self._ints(q_start, (n + 1,), "q_start") if q_start is not None else None
-        groups = 0
+        if q_start is not None:
+            ps = self._ints(q_start, (n + 1,), "q_start")
         if prefix_table is not None:
-            if prefix_table.dim() != 2:
-                raise ValueError("prefix_table: int32 [prefixes][pages] is required")
-            groups = prefix_table.shape[0]
-            prefix = B.verkv_span(self._ints(prefix_table, tuple(prefix_table.shape), "prefix_table"), groups,
-                                  prefix_table.shape[1], self._ints(prefix_lengths, (groups,), "prefix_lengths"),
-                                  max_prefix)
-        pg = self._ints(group_start, (groups + 1,), "group_start") if group_start is not None else None
-        po = pl = None
+            at, groups, stride = self._table(prefix_table, "prefix_table")
+            prefix = B.verkv_span(at, groups, stride, self._ints(prefix_lengths, (groups,), "prefix_lengths"), max_prefix)
+        if group_start is not None:
+            pg = self._ints(group_start, (groups + 1,), "group_start")
         if prior is not None:
-            for t, s, name in ((prior[0], tokens * self.hq * self.d, "prior o"), (prior[1], tokens * self.hq, "prior lse")):
-                if t.dtype != torch.float32 or t.device != self.dev or t.numel() != s or not t.is_contiguous():
-                    raise ValueError(f"{name}: a contiguous float32 tensor of {s} values on {self.dev} is required")
-            po, pl = prior[0].data_ptr(), prior[1].data_ptr()
+            o, l = prior
+            for t, size, name in ((o, tokens * hq * self.d, "prior o"), (l, tokens * hq, "prior lse")):
+                if t.dtype is not torch.float32 or t.device != dev or t.numel() != size or not t.is_contiguous():
+                    raise ValueError(f"{name}: a contiguous float32 tensor of {size} values on {dev} is required")
+            po, pl = o.data_ptr(), l.data_ptr()
+        shape = (tokens, hq, self.d)
         if out is None:
-            out = torch.empty((tokens, self.hq, self.d), dtype=self.dtype, device=self.dev)
-        elif out.dtype != self.dtype or out.device != self.dev or tuple(out.shape) != (tokens, self.hq, self.d) or not out.is_contiguous():
-            raise ValueError(f"out: a contiguous {self.dtype} [{tokens}][{self.hq}][{self.d}] tensor on {self.dev} is required")
+            out = torch.empty(shape, dtype=self.dtype, device=dev)
+        elif out.dtype is not self.dtype or out.device != dev or out.shape != shape or not out.is_contiguous():
+            raise ValueError(f"out: a contiguous {self.dtype} {list(shape)} tensor on {dev} is required")
         if lse is None:
-            lse = torch.empty((tokens, self.hq), dtype=torch.float32, device=self.dev)
-        elif lse.dtype != torch.float32 or lse.device != self.dev or tuple(lse.shape) != (tokens, self.hq) or not lse.is_contiguous():
-            raise ValueError(f"lse: a contiguous float32 [{tokens}][{self.hq}] tensor on {self.dev} is required")
+            lse = torch.empty((tokens, hq), dtype=torch.float32, device=dev)
+        elif lse.dtype is not torch.float32 or lse.device != dev or lse.shape != (tokens, hq) or not lse.is_contiguous():
+            raise ValueError(f"lse: a contiguous float32 [{tokens}][{hq}] tensor on {dev} is required")
         pages = self._layer(layer)
-        if tokens:
-            ws, nbytes = self._space(n, groups, tokens)
-            B.verkv_paged_attend(self.ctx, pages, n, tokens, rq, ps, own, prefix, pg, scale, po, pl,
-                                 out.data_ptr(), lse.data_ptr(), ws, nbytes)
+        if not tokens:
+            return out, lse
+        ws, nbytes = self._space(n, groups, tokens)
+        st = self._lib.verkv_paged_attend(self.ctx, pages, n, tokens, rq, ps, own, prefix, pg, scale, po, pl,
+                                          out.data_ptr(), lse.data_ptr(), ws, nbytes)
+        if st:
+            self._fail(st)
         return out, lse
 
     def _space(self, seqs, groups, tokens):
-        need = self._needs.get((seqs, groups, tokens))
+        key = (seqs, groups, tokens)
+        need = self._needs.get(key)
         if need is None:
-            need = self._needs[seqs, groups, tokens] = B.verkv_paged_workspace_size(self.shape, seqs, groups, tokens)
+            need = B.verkv_paged_workspace_size(self.shape, seqs, groups, tokens)
             if need == 0:
                 raise B.VerkvError(B.VERKV_EINVAL, "too many sequences, prefixes or queries")
-        if not self._spaces or self._spaces[-1].numel() < need:
+            self._needs[key] = need
+        if need > self._space_bytes:
             self._spaces.append(torch.empty(need, dtype=torch.uint8, device=self.dev))
-        ws = self._spaces[-1]
-        return ws.data_ptr(), ws.numel()
+            self._space_at, self._space_bytes = self._spaces[-1].data_ptr(), need
+        return self._space_at, self._space_bytes
 
     def sync(self):
         """Wait, and raise what the device has reported since the last call."""
@@ -277,6 +285,3 @@ class PagedKV:
             self.close()
         except Exception:  # noqa: BLE001 -- interpreter shutdown
             pass
-
-
-assert ctypes.sizeof(B.verkv_span) == 32
