@@ -81,7 +81,8 @@ __device__ __forceinline__ int page_ids(const PagedArgs &a, const int32_t *row, 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(PG_NT, PG_CTAS)
-    k_paged(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const __grid_constant__ CUtensorMap map) {
+    k_paged(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int wait_first,
+            const __grid_constant__ CUtensorMap map) {
     using LY = PagedLayout<D>;
     constexpr int KS = D / 16, NS = LY::NS;
     extern __shared__ __align__(1024) unsigned char pg_smem[];
@@ -111,7 +112,8 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
 #pragma unroll 1
         for (int dry = 1; dry >= 0; --dry) {
             if (!dry) {
-                pdl_wait();
+                // (k_paged_wide lets this kernel start when it has waited itself)
+                if (wait_first) pdl_wait();
                 pdl_trigger();
             }
             wk.start(a, l, blockIdx.x, dry != 0);
@@ -388,8 +390,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[k]);
         }
-        // The caller's stream may go on only when the launch before this one is done.
-        pdl_wait();
+        pdl_wait();  // the launch before this one is done when this one is
     }
     __syncthreads();
 }
@@ -533,14 +534,14 @@ cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long l
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, int dtype, int d,
+cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype, int d,
                          cudaStream_t s) {
 #define VERKV_PAGED(TT, DT, DD)                                                            \
     if (dtype == DT && d == DD) {                                                          \
         const size_t smem = PagedLayout<DD>::BYTES;                                        \
         const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD>, smem);            \
         if (e != cudaSuccess) return e;                                                    \
-        return launch_pdl(k_paged<TT, DD>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, map); \
+        return launch_pdl(k_paged<TT, DD>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
     }
     VERKV_PAGED(PgBf16, VERKV_BF16, 128) VERKV_PAGED(PgBf16, VERKV_BF16, 64)
     VERKV_PAGED(PgF16, VERKV_F16, 128) VERKV_PAGED(PgF16, VERKV_F16, 64)

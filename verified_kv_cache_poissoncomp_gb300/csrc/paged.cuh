@@ -54,6 +54,7 @@ struct PagedLine {
     int tt_shift;               // log2 of the query tokens of a row tile, tt
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
+    int steps, tall;            // (host: at most so many steps; tiles of 256 rows)
     int2 *rec;                  // {per, 0}, then {work before, units before} of each segment; per 0: no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
     float *part_o;
@@ -81,12 +82,11 @@ constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
 constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
 
 cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long long rows, int d, int box_rows);
-cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, int dtype, int d,
+// wait_first false: the launch before it on the stream is this call's k_paged_wide, which it need not
+// wait for to begin.
+cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype, int d,
                          cudaStream_t s);
-// wait_first false: the launch before it on the stream is this call's k_paged, which it need not wait
-// for to begin.
-cudaError_t launch_paged_wide(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype,
-                              int d, cudaStream_t s);
+cudaError_t launch_paged_wide(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, int dtype, int d, cudaStream_t s);
 struct PagedLines {
     PagedLine l[PAGED_LINES];
 };

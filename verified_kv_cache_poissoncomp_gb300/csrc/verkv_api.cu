@@ -468,6 +468,7 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
         if (l.with[x]) level(a.level[x]);
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
     if (steps >= (1LL << 31) || units + l.ctas >= (1LL << 31)) return false;
+    l.steps = (int)steps;
     l.slots = (int)(units + l.ctas);
     auto take = [&](size_t bytes) {
         unsigned char *p = ws + off;
@@ -478,6 +479,19 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     l.part_ml = (float *)take((size_t)l.slots * rows_tile * 2 * 4);
     l.part_o = (float *)take((size_t)l.slots * rows_tile * ctx->sh.head_dim * 4);
     return true;
+}
+
+// The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, so that in
+// turn each would leave the GPU idle while the other starts and ends.  Where k_paged has little to do
+// it gets a few SMs of its own beside the others (8 sequences behind 32K tokens: 64 -> XX us); where
+// it has much, it follows on all of them.  Costs are the measured us of a step: 1.0 of k_paged alone
+// on an SM, 1.5 or 2 of k_paged_wide with 128 or 256 rows.
+void paged_share(PagedLine &wide, PagedLine &own, int sms) {
+    const double w = wide.steps * (wide.tall ? 2.0 : 1.5), o = own.steps;
+    const int x = (int)(sms * o / (w + o)) + 1;
+    if (x > sms / 4) return;
+    own.ctas = std::min(own.ctas, x);
+    wide.ctas = std::min(wide.ctas, sms - x);
 }
 
 }  // namespace
@@ -1206,9 +1220,10 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         lines[0].tile_shift = log2_of(PAGED_TILE);
         lines[1].tile_shift = log2_of(PAGED_WIDE_TILE);
         lines[1].grouped = 1;
+        lines[1].tall = tall;
         bool ok = true;
-        if (few) ok &= paged_line(ctx, a, lines[0], PAGED_ROWS, std::min(ctx->sms * 2, PAGED_MAX_CTAS), (unsigned char *)workspace, off);
         if (many) ok &= paged_line(ctx, a, lines[1], tall ? 256 : 128, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
+        if (few) ok &= paged_line(ctx, a, lines[0], PAGED_ROWS, std::min(ctx->sms * 2, PAGED_MAX_CTAS), (unsigned char *)workspace, off);
         if (!ok) return fail(ctx, VERKV_EINVAL, "paged_attend: more than 2^31 steps of work in one call");
         if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
         CUtensorMap map;
@@ -1216,15 +1231,18 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
             return paged_tensor_map(&map, pages->kv, pages->dtype, (long long)pages->num_pages * a.hkv * pages->page_tokens,
                                     sh.head_dim, std::min(pages->page_tokens, tile));
         };
-        if (few) {
-            VERKV_CUDA(make_map(PAGED_TILE), "tensor map of the pages");
-            VERKV_CUDA(tracked(ctx, VERKV_K_PAGED, ctx->main, [&] { return launch_paged(a, lines[0], map, pages->dtype, sh.head_dim, ctx->main); }), "k_paged");
-        }
+        if (few && many) paged_share(lines[1], lines[0], ctx->sms);
         if (many) {
             VERKV_CUDA(make_map(PAGED_WIDE_TILE), "tensor map of the pages");
             VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_WIDE, ctx->main, [&] {
-                           return launch_paged_wide(a, lines[1], map, !few || ctx->prof_on, pages->dtype, sh.head_dim, ctx->main);
+                           return launch_paged_wide(a, lines[1], map, pages->dtype, sh.head_dim, ctx->main);
                        }), "k_paged_wide");
+        }
+        if (few) {
+            VERKV_CUDA(make_map(PAGED_TILE), "tensor map of the pages");
+            VERKV_CUDA(tracked(ctx, VERKV_K_PAGED, ctx->main, [&] {
+                           return launch_paged(a, lines[0], map, !many || ctx->prof_on, pages->dtype, sh.head_dim, ctx->main);
+                       }), "k_paged");
         }
     }
     VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_MERGE, ctx->main, [&] { return launch_paged_merge(a, both, pages->dtype, sh.head_dim, ctx->main); }), "k_paged_merge");
