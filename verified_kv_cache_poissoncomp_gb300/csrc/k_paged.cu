@@ -446,12 +446,12 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
             const PagedSeg sg = paged_segment(a, l, i, bad);
             const int j = t - sg.q0;
             if (j < 0 || j >= sg.qn || per <= 0) continue;  // (per 0: a bad segment, nothing was done)
-            const int nt = paged_row_tiles(sg, l), mt = j >> l.tt_shift, steps = paged_steps(sg, l, mt);
+            const int mt = j >> l.tt_shift, steps = paged_steps(sg, l, mt);
             if (steps == 0) continue;
-            const int w0 = before.x + head * paged_steps_before(sg, l, nt) + paged_steps_before(sg, l, mt);
+            const int w0 = before.x + paged_steps_before(sg, l, mt) * a.hkv + head * steps;
             const int c0 = (unsigned)w0 / (unsigned)per, c1 = (unsigned)(w0 + steps - 1) / (unsigned)per;
             const int in = ((j - (mt << l.tt_shift)) << a.g_shift) + g;
-            const int slot = clampi(c0 + before.y + head * nt + mt, 0, l.slots - 1);
+            const int slot = clampi(c0 + before.y + mt * a.hkv + head, 0, l.slots - 1);
             count[own] = clampi(c1 - c0 + 1, 0, l.slots - slot);
             rows[own] = 1 << (l.tt_shift + a.g_shift);
             grouped[own] = l.grouped != 0;

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     const uint32_t tm = *tmem_at;
     // S (and P over it) of chain i in columns 128 i .., O in 256 + 128 i ..
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = paged_wait(bar, parity, abort);
+        const bool ok = paged_wait(smem_addr(bar), parity, abort);
         if (__all_sync(0xFFFFFFFFu, ok)) return true;
         if (lane == 0) {
             *abort = 1;
@@ -247,8 +247,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
             constexpr uint32_t IS = mma_desc(128, 128, W::BF, false), IO = mma_desc(128, D, W::BF, true);
             const uint32_t st = tm + i * 128, ot = tm + 256 + i * 128;
             auto await = [&](uint64_t *bar, uint32_t parity) -> bool {
-                if (mbar_try_wait(bar, parity & 1u)) return true;
-                if (paged_wait(bar, parity, abort)) return true;
+                if (paged_wait(smem_addr(bar), parity, abort)) return true;
                 *abort = 1;
                 raise_error(a.err, ERR_TIMEOUT);
                 return false;

@@ -5,10 +5,12 @@
 // its group) or a sequence's own pages (rows: its queries).  A segment splits into units: one KV
 // head and one tile of up to `tt` query tokens, all q_per_kv heads of each.  A unit's work is the
 // number of `tile`-token steps over what its last query sees.  All units' work, laid end to end
-// (segment, head, row tile, step), is cut into equal runs of `per` steps, one for each CTA, wherever
+// (segment, row tile, head, step), is cut into equal runs of `per` steps, one for each CTA, wherever
 // the cuts fall: however uneven the lengths are, no CTA has more than `per` steps, a long unit is shared by many CTAs and a CTA takes many short ones.  Lengths are read on
 // the device, so a captured graph follows them.  The piece of unit u in run c goes to the partial
-// slot c + u: walking the line, each step to the next piece raises exactly one of the two.
+// slot c + u: walking the line, each step to the next piece raises exactly one of the two.  Row tiles
+// come before heads so that the CTAs which read the same K and V for other rows do so at about the
+// same time, from the L2 cache (heads first, 1024 rows read a 134 MB prefix four times from memory).
 #pragma once
 
 #include <cuda.h>
@@ -258,24 +260,24 @@ struct PagedWalk {
             load(a, l);
         }
         int r = w - Wx;
-        head = (unsigned)r / (unsigned)per_head;
-        r -= head * per_head;
         m = 0;
         int steps = paged_steps(s, l, 0);
         if (!s.own) {
-            m = (unsigned)r / (unsigned)steps;
-            r -= m * steps;
+            m = (unsigned)r / (unsigned)(steps * a.hkv);
+            r -= m * steps * a.hkv;
         } else {
 #pragma unroll 1
-            while (r >= steps) {
-                r -= steps;
+            while (r >= steps * a.hkv) {
+                r -= steps * a.hkv;
                 if (++m >= nt) return false;  // lengths changed under the kernel
                 steps = paged_steps(s, l, m);
             }
         }
+        head = (unsigned)r / (unsigned)steps;
+        r -= head * steps;
         t0 = r;
         t1 = min(steps, r + (w1 - w));
-        slot = c + Ux + head * nt + m;
+        slot = c + Ux + m * a.hkv + head;
         w += t1 - t0;
         return true;
     }
@@ -320,18 +322,31 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Wait for phase `parity` of the barrier; false when *abort is set or the time is up.  The clock and
-// the flag are looked at between runs of polls only: with each poll they add 300 cycles to a wake-up.
-__device__ __forceinline__ bool paged_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity & 1u)
+        : "memory");
+    return done != 0;
+}
+
+// Wait for phase `parity` of the barrier at shared address `bar`; false when *abort is set or the time
+// is up.  The first poll is in line and the rest is a call: a warp that issues products or copies runs
+// between others that fill the instruction cache, and pays for each line of code it passes.
+static __device__ __noinline__ bool paged_wait_long(uint32_t bar, uint32_t parity, volatile int *abort) {
     unsigned long long t0 = 0;
     for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity & 1u)) return true;
+        for (int i = 0; i < 16; ++i)
+            if (mbar_poll(bar, parity)) return true;
         const unsigned long long t = globaltimer_ns();
         if (t0 == 0) t0 = t;
         if (*abort || t - t0 > TMA_WAIT_NS) return false;
     }
+}
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return mbar_poll(bar, parity) || paged_wait_long(bar, parity, abort);
 }
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {

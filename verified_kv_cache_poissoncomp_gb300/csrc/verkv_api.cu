@@ -481,15 +481,16 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     return true;
 }
 
-// The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, so that in
-// turn each would leave the GPU idle while the other starts and ends.  Where k_paged has little to do
-// it gets a few SMs of its own beside the others (8 sequences behind 32K tokens: 64 -> XX us); where
-// it has much, it follows on all of them.  Costs are the measured us of a step: 1.0 of k_paged alone
-// on an SM, 1.5 or 2 of k_paged_wide with 128 or 256 rows.
+// The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, so that one
+// after the other each leaves the GPU idle while it starts and ends, some 10 us.  Where k_paged's work
+// is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 64 -> 45 us, 64
+// sequences 86 -> 74); but alone on an SM it takes longer in all, so where its work would fill the
+// GPU for 30 us it follows on all of it (256 sequences: 178 against 201 us side by side).  Costs are
+// the measured us of a step: 0.8 of k_paged alone on an SM, 1.5 or 2 of k_paged_wide with 128 or 256 rows.
 void paged_share(PagedLine &wide, PagedLine &own, int sms) {
-    const double w = wide.steps * (wide.tall ? 2.0 : 1.5), o = own.steps;
+    const double w = wide.steps * (wide.tall ? 2.0 : 1.5), o = own.steps * 0.8;
     const int x = (int)(sms * o / (w + o)) + 1;
-    if (x > sms / 4) return;
+    if (x > sms / 2 || o > 30.0 * sms) return;
     own.ctas = std::min(own.ctas, x);
     wide.ctas = std::min(wide.ctas, sms - x);
 }
