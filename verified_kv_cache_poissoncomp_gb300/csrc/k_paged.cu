@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                 if (wait_first) pdl_wait();
                 pdl_trigger();
             }
-            wk.start(a, l, blockIdx.x, dry != 0);
+            // (the queries' place holds nothing yet)
+            wk.start(a, l, blockIdx.x, dry != 0, reinterpret_cast<int2 *>(pg_smem + LY::Q), NS * PG_R * LY::QROW / 8);
         }
         // The walk is one piece ahead of the copies, so that a piece's page ids are there when its
         // first step is.

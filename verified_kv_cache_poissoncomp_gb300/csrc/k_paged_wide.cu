@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(PW_NT, 1)
                 pdl_wait();
                 pdl_trigger();
             }
-            wk.start(a, l, blockIdx.x, dry != 0);
+            // (the chains' states have no use for their place yet)
+            wk.start(a, l, blockIdx.x, dry != 0, reinterpret_cast<int2 *>(ml), 2 * 128);
         }
         const int box = min(1 << a.page_shift, PAGED_WIDE_TILE);
         int j = 0, np = 0;  // slots and pieces so far

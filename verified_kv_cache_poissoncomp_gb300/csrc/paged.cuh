@@ -57,7 +57,7 @@ struct PagedLine {
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
     int steps, tall;            // (host: at most so many steps; tiles of 256 rows)
-    int2 *rec;                  // {per, 0}, then {work before, units before} of each segment; per 0: no work
+    int2 *rec;                  // {per, 0}, then {work before, units before} of each segment with work; per 0: a bad segment, no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
     float *part_o;
     float *part_ml;             // [slots][tt * G][2]: running maximum (log2 units) and sum
@@ -179,74 +179,69 @@ struct PagedWalk {
         per_head = paged_steps_before(s, l, nt);
     }
 
-    // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also
-    // writes the line's record for the merge and reports bad segments, unless `dry`.  Two passes of
-    // the same loop: for the whole line's steps, and then for the place.
-    __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c, bool dry) {
+    // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also writes
+    // how long a run is and reports bad segments, unless `dry`.  First the whole
+    // line's steps, keeping each segment's in shared memory (`cap` of them) as it goes, then the place.
+    __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c, bool dry, int2 *cache, int cap) {
         const int lane = threadIdx.x & 31;
         n = paged_segments(a, l);
         seg = n;
         w = w1 = 0;
         bool bad = false;
+        int total = 0;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) {
+            const PagedSeg g = paged_segment(a, l, i, bad);
+            const int t = paged_row_tiles(g, l), h = paged_steps_before(g, l, t);
+            total += h;
+            if (i < cap) cache[i] = make_int2(h, t);
+        }
+        total = __reduce_add_sync(0xFFFFFFFFu, total) * a.hkv;
+        bad = __any_sync(0xFFFFFFFFu, bad);
+        const int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
+        if (c == 0 && !dry && lane == 0) {
+            l.rec[0] = make_int2(per, 0);
+            if (bad) raise_error(a.err, ERR_PAGE);
+        }
+        if (bad) return;
+        w = (int)min((long long)total, (long long)c * per);
+        w1 = min(total, w + per);
+        if (w >= w1) return;
+        int wx = 0, ux = 0;
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-            int wx = 0, ux = 0;
-#pragma unroll 1
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                PagedSeg g = {};
-                int gt = 0, gh = 0;  // row tiles, steps of one head
-                if (i0 + lane < n) {
-                    g = paged_segment(a, l, i0 + lane, bad);
-                    gt = paged_row_tiles(g, l);
-                    gh = paged_steps_before(g, l, gt);
-                }
-                const int mw = gh * a.hkv, mu = gt * a.hkv;
-                if (pass == 0) {
-                    wx += __reduce_add_sync(0xFFFFFFFFu, mw);
-                    continue;
-                }
-                int sw = mw, su = mu;  // inclusive sums over the lanes
-#pragma unroll 1
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int pw = __shfl_up_sync(0xFFFFFFFFu, sw, o), pu = __shfl_up_sync(0xFFFFFFFFu, su, o);
-                    if (lane >= o) {
-                        sw += pw;
-                        su += pu;
-                    }
-                }
-                const int ew = wx + sw - mw, eu = ux + su - mu;
-                if (c == 0 && !dry && i0 + lane < n) l.rec[1 + i0 + lane] = make_int2(ew, eu);
-                const unsigned hit = __ballot_sync(0xFFFFFFFFu, w < w1 && w >= ew && w < ew + mw);
-                if (hit) {  // the run begins in this lane's segment
-                    const int at = __ffs(hit) - 1;
-                    seg = i0 + at;
-                    Wx = __shfl_sync(0xFFFFFFFFu, ew, at);
-                    Ux = __shfl_sync(0xFFFFFFFFu, eu, at);
-                    s.q0 = __shfl_sync(0xFFFFFFFFu, g.q0, at);
-                    s.qn = __shfl_sync(0xFFFFFFFFu, g.qn, at);
-                    s.len = __shfl_sync(0xFFFFFFFFu, g.len, at);
-                    s.row = __shfl_sync(0xFFFFFFFFu, g.row, at);
-                    s.own = __shfl_sync(0xFFFFFFFFu, (int)g.own, at) != 0;
-                    nt = __shfl_sync(0xFFFFFFFFu, gt, at);
-                    per_head = __shfl_sync(0xFFFFFFFFu, gh, at);
-                    if (c != 0) return;
-                }
-                wx += __shfl_sync(0xFFFFFFFFu, sw, 31);
-                ux += __shfl_sync(0xFFFFFFFFu, su, 31);
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            int gh = 0, gt = 0;  // steps of one head, row tiles
+            if (i < cap && i < n) {
+                gh = cache[i].x;
+                gt = cache[i].y;
+            } else if (i < n) {
+                const PagedSeg g = paged_segment(a, l, i, bad);
+                gt = paged_row_tiles(g, l);
+                gh = paged_steps_before(g, l, gt);
             }
-            if (pass == 0) {
-                bad = __any_sync(0xFFFFFFFFu, bad);
-                const int per = bad ? 0 : (int)max(1u, ((unsigned)wx + l.ctas - 1) / (unsigned)l.ctas);
-                if (c == 0 && lane == 0 && !dry) {
-                    l.rec[0] = make_int2(per, 0);
-                    if (bad) raise_error(a.err, ERR_PAGE);
+            const int mw = gh * a.hkv, mu = gt * a.hkv;
+            int sw = mw, su = mu;  // inclusive sums over the lanes
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int pw = __shfl_up_sync(0xFFFFFFFFu, sw, o), pu = __shfl_up_sync(0xFFFFFFFFu, su, o);
+                if (lane >= o) {
+                    sw += pw;
+                    su += pu;
                 }
-                if (!bad) {
-                    w = (int)min((long long)wx, (long long)c * per);
-                    w1 = min(wx, w + per);
-                }
-                if (bad || (w >= w1 && c != 0)) return;
             }
+            const int ew = wx + sw - mw, eu = ux + su - mu;
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, w < w1 && w >= ew && w < ew + mw);
+            if (hit) {  // the run begins in this lane's segment
+                const int at = __ffs(hit) - 1;
+                seg = i0 + at - 1;  // (next() goes on to it)
+                Wx = __shfl_sync(0xFFFFFFFFu, ew, at);
+                Ux = __shfl_sync(0xFFFFFFFFu, eu, at);
+                per_head = nt = 0;
+                return;
+            }
+            wx += __shfl_sync(0xFFFFFFFFu, sw, 31);
+            ux += __shfl_sync(0xFFFFFFFFu, su, 31);
         }
     }
 
@@ -259,6 +254,8 @@ struct PagedWalk {
             Ux += nt * a.hkv;
             load(a, l);
         }
+        // The run in which a segment begins writes its record for the merge.
+        if (w == Wx && (threadIdx.x & 31) == 0) l.rec[1 + seg] = make_int2(Wx, Ux);
         int r = w - Wx;
         m = 0;
         int steps = paged_steps(s, l, 0);
