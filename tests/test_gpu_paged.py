@@ -107,6 +107,15 @@ def test_one_prefix_for_all(seqs, prefix):
     Case([(7 * i) % 90 for i in range(seqs)], prefixes=[prefix], h=1 + (seqs < 9), g=4, pt=64).check()
 
 
+@pytest.mark.parametrize("rows,lengths,prefix", [
+    (4, [4000, 9000, 2500, 0, 7001], 0), (4, [3000] * 3, 40001), (16, [2500] * 2, 30001), (32, [2000] * 3, 30001),
+    (24, [9000, 1, 5000, 12000], 0), (64, [1000] * 2, 30001), (200, [6000, 300, 9001], 0), (400, [200], 30001)])
+def test_long_runs(rows, lengths, prefix):
+    # every CTA takes many steps of several units, and units end inside its run
+    qs = max(1, rows // 4 // (len(lengths) if prefix else 1))
+    Case(lengths, qs=[qs] * len(lengths), prefixes=[prefix] if prefix else (), h=8, g=4, d=64, pt=64).check()
+
+
 @pytest.mark.parametrize("d,dtype,qs", [(64, BF, 1), (128, HF, 1), (128, BF, 3), (64, HF, 5)])
 def test_groups_with_their_own_prefixes(d, dtype, qs):
     # groups of 40, 0, 1, 25 sequences; a prefix without tokens, prefixes without sequences

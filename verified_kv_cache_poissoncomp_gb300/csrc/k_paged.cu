@@ -2,14 +2,14 @@
 //
 //   o = sum_i 2^(l_i - m) v_i / sum_i 2^(l_i - m),   l_i = q . k_i scale log2(e), m the running maximum
 //
-// k_paged: up to 16 query rows (query tokens x heads of one KV head) against a run of cached tokens.
+// k_paged: 16 or 32 query rows (query tokens x heads of one KV head) against a run of cached tokens.
 // Bound by the bytes of K and V: a decode step has q_per_kv rows a sequence, a few flops per byte.
 // One warp walks the CTA's run of the line (paged.cuh) and copies 64-token steps of K and V into
 // a shared-memory ring by TMA (boxes of one page's tokens x 64 channels, 128-byte swizzle), with a
 // unit's queries beside its first step; what a step is (which rows, which tokens, whether a unit
 // begins or ends with it) travels with it, so one warp's walk drives the CTA and runs ahead of it.
-// Four warps take 16 tokens of a step each: S = Q K^T with the rows as the m16 of mma.m16n8k16 (K by
-// ldmatrix), the softmax in registers -- each warp keeps its own running maximum and sum and rescales
+// Four warps take 16 tokens of a step each (with 32 rows: two take each half of the rows, 32 tokens
+// each): S = Q K^T with the rows as the m16 of mma.m16n8k16 (K by ldmatrix), the softmax in registers -- each warp keeps its own running maximum and sum and rescales
 // only when some row's maximum rises -- and P, already in the A operand's layout, times V (ldmatrix,
 // transposed).  At a unit's end the four warps' states are joined in the step's own shared memory,
 // which nothing reads any more, and written as one partial.
@@ -30,7 +30,6 @@ namespace {
 
 constexpr int PG_CONS = 4;                     // consumer warps: 16 tokens of a step each
 constexpr int PG_NT = 32 * (PG_CONS + 1);      // and one warp that walks and copies
-constexpr int PG_R = PAGED_ROWS;               // rows of a unit: the m16 of an mma
 constexpr int PG_CTAS = 2;                     // an SM
 
 struct StepDesc {
@@ -38,24 +37,28 @@ struct StepDesc {
     int valid;       // tokens of the step that some row of the unit sees
     int tok0;        // the step's first token
     int rows;        // real rows
+    int q;           // where the unit's queries are: slot of their ring
     int lim0, limd;  // tokens the tile's first query sees, and how many more each next one does
     int slot;        // partial slot, or -1
 };
 enum { PG_FIRST = 1, PG_LAST = 2, PG_END = 4 };
 
-template <int D>
+// RH: halves of 16 rows.
+template <int D, int RH>
 struct PagedLayout {
     static constexpr int HALVES = D / 64;
     static constexpr int BOX = PAGED_TILE * 128;
     static constexpr int STAGE = 2 * HALVES * BOX;
     static constexpr int NS = D == 128 ? 3 : 6;
-    static constexpr int QROW = 2 * D + 16;                 // pitch: ldmatrix's 8 rows in different banks
-    static constexpr int Q = NS * STAGE;                    // [NS][PG_R][QROW]
-    static constexpr int ML = Q + NS * PG_R * QROW;         // float [4][PG_R][2]
-    static constexpr int DESC = ML + PG_CONS * PG_R * 2 * 4;
+    static constexpr int R = 16 * RH;
+    static constexpr int QN = RH == 1 ? NS : 2;                  // units whose queries are held
+    static constexpr int QROW = 2 * D + (RH == 1 ? 16 : 0);      // (padded where there is room: ldmatrix's banks)
+    static constexpr int Q = NS * STAGE;                         // [QN][R][QROW]
+    static constexpr int ML = Q + QN * R * QROW;                 // float [4][16][2]
+    static constexpr int DESC = ML + PG_CONS * 16 * 2 * 4;
     static constexpr int BARS = (DESC + NS * (int)sizeof(StepDesc) + 7) / 8 * 8;  // full, empty [NS], join
     static constexpr int BYTES = BARS + (2 * NS + 1) * 8 + 8;
-    static_assert(PG_CONS * PG_R * D * 4 <= STAGE, "a stage holds the four warps' sums");
+    static_assert(PG_CONS * 16 * D * 4 <= STAGE, "a stage holds the four warps' sums");
     static_assert((BYTES + 1024) * PG_CTAS <= 228 * 1024, "CTAs an SM");
 };
 
@@ -79,12 +82,12 @@ __device__ __forceinline__ int page_ids(const PagedArgs &a, const int32_t *row, 
     return id;
 }
 
-template <typename T, int D>
+template <typename T, int D, int RH>
 __global__ void __launch_bounds__(PG_NT, PG_CTAS)
     k_paged(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int wait_first,
             const __grid_constant__ CUtensorMap map) {
-    using LY = PagedLayout<D>;
-    constexpr int KS = D / 16, NS = LY::NS;
+    using LY = PagedLayout<D, RH>;
+    constexpr int KS = D / 16, NS = LY::NS, R = LY::R;
     extern __shared__ __align__(1024) unsigned char pg_smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(pg_smem + LY::BARS), *empty = full + NS, *join = empty + NS;
     volatile int *abort = reinterpret_cast<volatile int *>(join + 1);
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                 pdl_trigger();
             }
             // (the queries' place holds nothing yet)
-            wk.start(a, l, blockIdx.x, dry != 0, reinterpret_cast<int2 *>(pg_smem + LY::Q), NS * PG_R * LY::QROW / 8);
+            wk.start(a, l, blockIdx.x, dry != 0, reinterpret_cast<int2 *>(pg_smem + LY::Q), LY::QN * R * LY::QROW / 8);
         }
         // The walk is one piece ahead of the copies, so that a piece's page ids are there when its
         // first step is.
@@ -141,7 +144,8 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         };
         Piece cur = {}, nxt = {};
         bool have = true, go = true;
-        int j = 0;
+        int j = 0, np = 0;      // steps and pieces so far
+        int begun[2] = {-1, -1};  // first steps of the last two pieces
         while (have && go) {
             have = fetch(nxt);
 #pragma unroll 1
@@ -156,12 +160,22 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                     cur.ids = page_ids(a, cur.row, p0, cur.vis);
                 }
                 const bool first = t == cur.t0;
+                if (first && LY::QN < NS) {
+                    // The queries' slot: the piece before the last one has begun to be worked on.  (Of a step
+                    // NS back that is known, and its barrier may be phases ahead.)
+                    const int b = begun[0];
+                    if (b >= 0 && b > j - NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[b % NS], (uint32_t)((b / NS) & 1), abort));
+                    if (!go) break;
+                    begun[0] = begun[1];
+                    begun[1] = j;
+                }
                 if (lane == 0) {
                     StepDesc s;
                     s.flags = (first ? PG_FIRST : 0) | (t + 1 == cur.t1 ? PG_LAST : 0);
                     s.valid = valid;
                     s.tok0 = tok0;
                     s.rows = cur.rows;
+                    s.q = np % LY::QN;
                     s.lim0 = cur.lim0;
                     s.limd = cur.limd;
                     s.slot = cur.slot;
@@ -180,10 +194,11 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                 }
                 if (first && lane < cur.rows) {
                     const int jj = lane >> a.g_shift, hh = (cur.head << a.g_shift) + lane - (jj << a.g_shift);
-                    bulk_g2s(pg_smem + LY::Q + (k * PG_R + lane) * LY::QROW, a.q + (cur.q0 + jj) * a.q_ts + hh * a.q_hs, 2 * D, &full[k]);
+                    bulk_g2s(pg_smem + LY::Q + (np % LY::QN * R + lane) * LY::QROW, a.q + (cur.q0 + jj) * a.q_ts + hh * a.q_hs, 2 * D, &full[k]);
                 }
                 __syncwarp();
             }
+            if (cur.t0 < cur.t1) ++np;
             cur = nxt;
         }
         if (go) {  // tell the consumers that the run is over
@@ -203,7 +218,10 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         }
         __syncwarp();
     } else {
-        const int g = lane >> 2, t = lane & 3, mi = lane >> 3, ri = lane & 7, w0 = warp * 16;
+        const int g = lane >> 2, t = lane & 3, mi = lane >> 3, ri = lane & 7;
+        const int rb = RH == 1 ? 0 : (warp >> 1) * 16;            // this warp's rows
+        const int wt = RH == 1 ? warp * 16 : (warp & 1) * 32;     // and tokens of a step
+        constexpr int NW = PG_CONS / RH;                           // warps with the same rows
         uint32_t qf[KS][4];
         float o[D / 8][4], mx[2], sum[2];
         int lim[2];
@@ -221,7 +239,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         // round could write: valid is 64.)
         for (int j = -1;; ++j) {
             const int k = j < 0 ? 0 : j % NS;
-            StepDesc s = {PG_FIRST, PAGED_TILE, 0, 0, 0, 0, -1};
+            StepDesc s = {PG_FIRST, PAGED_TILE, 0, R, 0, 0, 0, -1};
             if (j >= 0) {
                 const bool ok = mbar_wait_or_abort(&full[k], (uint32_t)((j / NS) & 1), abort);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -236,12 +254,12 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
             }
             unsigned char *st = pg_smem + (size_t)k * LY::STAGE;
             if (s.flags & PG_FIRST) {
-                const uint32_t qb = smem_addr(pg_smem + LY::Q) + (k * PG_R + (mi & 1) * 8 + ri) * LY::QROW + (mi >> 1) * 16;
+                const uint32_t qb = smem_addr(pg_smem + LY::Q) + (s.q * R + rb + (mi & 1) * 8 + ri) * LY::QROW + (mi >> 1) * 16;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) ldsm_x4(qf[ks], qb + ks * 32);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = g + 8 * e;
+                    const int r = rb + g + 8 * e;
                     lim[e] = r < s.rows ? s.lim0 + s.limd * (r >> a.g_shift) : 0;
                     mx[e] = -INFINITY;
                     sum[e] = 0.0f;
@@ -251,7 +269,9 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
             }
-            if (w0 < s.valid) {
+#pragma unroll 1
+            for (int w0 = wt; w0 < wt + 16 * RH; w0 += 16) {
+                if (w0 >= s.valid || rb >= s.rows) break;
                 const uint32_t kb = smem_addr(st), vb = kb + LY::HALVES * LY::BOX;
                 if (w0 + 16 > s.valid) {
                     // V rows that nothing sees may hold anything, NaN too: a weight of 0 would keep it
@@ -348,7 +368,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                 for (int e = 0; e < 2; ++e) {
                     sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
                     sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
-                    if (t == 0) *reinterpret_cast<float2 *>(ml + (warp * PG_R + g + 8 * e) * 2) = make_float2(mx[e], sum[e]);
+                    if (t == 0) *reinterpret_cast<float2 *>(ml + (warp * 16 + g + 8 * e) * 2) = make_float2(mx[e], sum[e]);
                 }
                 if (!cons_sync()) break;  // and no warp reads the slot's K and V any more
                 float *buf = reinterpret_cast<float *>(st);
@@ -356,31 +376,33 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                 for (int e = 0; e < 2; ++e) {
                     const int r = g + 8 * e;
                     float m = -INFINITY, z = 0.0f;
+                    const float *mz = ml + (rb / 16 * NW * 16 + r) * 2;  // of the warps with these rows
 #pragma unroll
-                    for (int w = 0; w < PG_CONS; ++w) m = fmaxf(m, ml[(w * PG_R + r) * 2]);
+                    for (int w = 0; w < NW; ++w) m = fmaxf(m, mz[w * 32]);
                     const float ms = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                    for (int w = 0; w < PG_CONS; ++w) z += ml[(w * PG_R + r) * 2 + 1] * exp2_fast(ml[(w * PG_R + r) * 2] - ms);
-                    if (r < s.rows) {
+                    for (int w = 0; w < NW; ++w) z += mz[w * 32 + 1] * exp2_fast(mz[w * 32] - ms);
+                    if (rb + r < s.rows) {
                         const float f = exp2_fast(mx[e] - ms);
 #pragma unroll
                         for (int n = 0; n < D / 8; ++n)
-                            *reinterpret_cast<float2 *>(buf + (warp * PG_R + r) * D + ((n * 8 + 2 * t) ^ (g << 3))) =
+                            *reinterpret_cast<float2 *>(buf + (warp * 16 + r) * D + ((n * 8 + 2 * t) ^ (g << 3))) =
                                 make_float2(o[n][2 * e] * f, o[n][2 * e + 1] * f);
-                        if (t == 0 && warp == 0 && s.slot >= 0)
-                            *reinterpret_cast<float2 *>(l.part_ml + ((long long)s.slot * PG_R + r) * 2) = make_float2(m, z);
+                        if (t == 0 && warp % NW == 0 && s.slot >= 0)
+                            *reinterpret_cast<float2 *>(l.part_ml + ((long long)s.slot * R + rb + r) * 2) = make_float2(m, z);
                     }
                 }
                 if (!cons_sync()) break;
                 if (s.slot >= 0) {
-                    float *po = l.part_o + (long long)s.slot * PG_R * D;
+                    float *po = l.part_o + (long long)s.slot * R * D;
 #pragma unroll 1
                     for (int x = tid * 4; x < s.rows * D; x += PG_CONS * 32 * 4) {
-                        const int y = x ^ (((x / D) & 7) << 3);  // as laid: 8 channels' groups turned by the row
+                        // as laid: 8 channels' groups turned by the row, and the half's first warp
+                        const int y = (x ^ (((x / D) & 7) << 3)) + x / (16 * D) * (NW - 1) * 16 * D;
                         float4 v = *reinterpret_cast<const float4 *>(buf + y);
 #pragma unroll
-                        for (int w = 1; w < PG_CONS; ++w) {
-                            const float4 u = *reinterpret_cast<const float4 *>(buf + w * PG_R * D + y);
+                        for (int w = 1; w < NW; ++w) {
+                            const float4 u = *reinterpret_cast<const float4 *>(buf + w * 16 * D + y);
                             v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
                         }
                         *reinterpret_cast<float4 *>(po + x) = v;
@@ -537,15 +559,18 @@ cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long l
 
 cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype, int d,
                          cudaStream_t s) {
-#define VERKV_PAGED(TT, DT, DD)                                                            \
-    if (dtype == DT && d == DD) {                                                          \
-        const size_t smem = PagedLayout<DD>::BYTES;                                        \
-        const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD>, smem);            \
+    const int rows = 1 << (l.tt_shift + a.g_shift);
+#define VERKV_PAGED(TT, DT, DD, RR)                                                        \
+    if (dtype == DT && d == DD && rows == 16 * RR) {                                       \
+        const size_t smem = PagedLayout<DD, RR>::BYTES;                                    \
+        const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD, RR>, smem);        \
         if (e != cudaSuccess) return e;                                                    \
-        return launch_pdl(k_paged<TT, DD>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
+        return launch_pdl(k_paged<TT, DD, RR>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
     }
-    VERKV_PAGED(PgBf16, VERKV_BF16, 128) VERKV_PAGED(PgBf16, VERKV_BF16, 64)
-    VERKV_PAGED(PgF16, VERKV_F16, 128) VERKV_PAGED(PgF16, VERKV_F16, 64)
+    VERKV_PAGED(PgBf16, VERKV_BF16, 128, 1) VERKV_PAGED(PgBf16, VERKV_BF16, 128, 2)
+    VERKV_PAGED(PgBf16, VERKV_BF16, 64, 1) VERKV_PAGED(PgBf16, VERKV_BF16, 64, 2)
+    VERKV_PAGED(PgF16, VERKV_F16, 128, 1) VERKV_PAGED(PgF16, VERKV_F16, 128, 2)
+    VERKV_PAGED(PgF16, VERKV_F16, 64, 1) VERKV_PAGED(PgF16, VERKV_F16, 64, 2)
 #undef VERKV_PAGED
     return cudaErrorInvalidValue;
 }

@@ -56,7 +56,7 @@ struct PagedLine {
     int tt_shift;               // log2 of the query tokens of a row tile, tt
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
-    int steps, tall;            // (host: at most so many steps; tiles of 256 rows)
+    int steps, units, tall;     // (host: at most so many steps and units; tiles of 256 rows)
     int2 *rec;                  // {per, 0}, then {work before, units before} of each segment with work; per 0: a bad segment, no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
     float *part_o;
@@ -79,7 +79,7 @@ struct PagedArgs {
 constexpr int PAGED_MAX_CTAS = 512;   // of k_paged
 constexpr int PAGED_WIDE_CTAS = 256;  // of k_paged_wide
 constexpr int PAGED_TILE = 64;        // tokens of a step of k_paged
-constexpr int PAGED_ROWS = 16;        // rows of its units
+constexpr int PAGED_ROWS = 32;        // most rows of its units (16 or 32)
 constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
 constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
 

@@ -435,10 +435,10 @@ constexpr int PAGED_WIDE_ROWS = PAGED_ROWS;
 
 // Upper bound of the partial rows of any call for up to these sizes.  Of one level: its queries'
 // rows q G, at most one ragged row tile a segment, and one slot a CTA.  A level in tiles of 128 rows
-// has more than 16 rows a segment on average, one in tiles of 256 more than 128: its ragged tiles add
-// at most 128 / 16 q G.
+// has more than 32 rows a segment on average, one in tiles of 256 more than 128: its ragged tiles add
+// at most 128 / 32 q G.
 int64_t paged_rows_bound(int64_t hkv, int64_t G, int64_t seqs, int64_t groups, int64_t q_tokens) {
-    return hkv * (2 * 9 * q_tokens * G + PAGED_ROWS * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * PAGED_ROWS +
+    return hkv * (2 * 5 * q_tokens * G + PAGED_ROWS * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * PAGED_ROWS +
            (int64_t)PAGED_WIDE_CTAS * 256;
 }
 bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_shape &sh) {
@@ -469,6 +469,7 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
     if (steps >= (1LL << 31) || units + l.ctas >= (1LL << 31)) return false;
     l.steps = (int)steps;
+    l.units = (int)units;
     l.slots = (int)(units + l.ctas);
     auto take = [&](size_t bytes) {
         unsigned char *p = ws + off;
@@ -486,9 +487,10 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
 // is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 64 -> 45 us, 64
 // sequences 86 -> 74); but alone on an SM it takes longer in all, so where its work would fill the
 // GPU for 30 us it follows on all of it (256 sequences: 178 against 201 us side by side).  Costs are
-// the measured us of a step: 0.8 of k_paged alone on an SM, 1.5 or 2 of k_paged_wide with 128 or 256 rows.
+// the measured us of a step: 0.8 of k_paged alone on an SM, and 1.2 a unit; 1.5 or 2 of k_paged_wide with
+// 128 or 256 rows.
 void paged_share(PagedLine &wide, PagedLine &own, int sms) {
-    const double w = wide.steps * (wide.tall ? 2.0 : 1.5), o = own.steps * 0.8;
+    const double w = wide.steps * (wide.tall ? 2.0 : 1.5), o = own.steps * 0.8 + own.units * 1.2;
     const int x = (int)(sms * o / (w + o)) + 1;
     if (x > sms / 2 || o > 30.0 * sms) return;
     own.ctas = std::min(own.ctas, x);
@@ -1224,7 +1226,8 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         lines[1].tall = tall;
         bool ok = true;
         if (many) ok &= paged_line(ctx, a, lines[1], tall ? 256 : 128, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
-        if (few) ok &= paged_line(ctx, a, lines[0], PAGED_ROWS, std::min(ctx->sms * 2, PAGED_MAX_CTAS), (unsigned char *)workspace, off);
+        const int64_t rows_few = std::max(lines[0].with[0] ? rows_prefix : 0, lines[0].with[1] ? rows_own : 0);
+        if (few) ok &= paged_line(ctx, a, lines[0], rows_few <= 16 ? 16 : PAGED_ROWS, std::min(ctx->sms * 2, PAGED_MAX_CTAS), (unsigned char *)workspace, off);
         if (!ok) return fail(ctx, VERKV_EINVAL, "paged_attend: more than 2^31 steps of work in one call");
         if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
         CUtensorMap map;
