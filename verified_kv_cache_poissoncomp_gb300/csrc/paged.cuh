@@ -56,7 +56,8 @@ struct PagedLine {
     int tt_shift;               // log2 of the query tokens of a row tile, tt
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
-    int steps, units, tall;     // (host: at most so many steps and units; tiles of 256 rows)
+    int tall;                   // (host: tiles of 256 rows)
+    double cost;                // (host: us of one SM)
     int2 *rec;                  // {per, 0}, then {work before, units before} of each segment with work; per 0: a bad segment, no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
     float *part_o;

@@ -430,15 +430,19 @@ constexpr int PAGED_MAX_SEGMENTS = 65536;  // sequences or prefixes of a call
 // Rows of a segment, on average and rounded up.
 int64_t paged_rows(int64_t q_tokens, int64_t segments, int G) { return (q_tokens + segments - 1) / segments * G; }
 
-// A level whose segments have more rows than this goes through k_paged_wide, else k_paged.
-constexpr int PAGED_WIDE_ROWS = PAGED_ROWS;
+// Which kernel a level goes through, by the rows of its segments.  Prefixes of up to 16 rows and own
+// tokens of up to 32: k_paged; more: k_paged_wide.  (32 rows of a 32K prefix: k_paged 52 us, reading at
+// 4.5 TB/s for its arithmetic, k_paged_wide 44; own tokens of 32 sequences of 18 rows, up to 4096 each:
+// k_paged 61, k_paged_wide, whose 128 rows are then mostly empty, 94.)
+bool paged_wide_prefix(int64_t rows) { return rows > PAGED_ROWS / 2; }
+bool paged_wide_own(int64_t rows) { return rows > PAGED_ROWS; }
 
 // Upper bound of the partial rows of any call for up to these sizes.  Of one level: its queries'
 // rows q G, at most one ragged row tile a segment, and one slot a CTA.  A level in tiles of 128 rows
-// has more than 32 rows a segment on average, one in tiles of 256 more than 128: its ragged tiles add
-// at most 128 / 32 q G.
+// has more than 16 rows a segment on average, one in tiles of 256 more than 128: its ragged tiles add
+// at most 128 / 16 q G.
 int64_t paged_rows_bound(int64_t hkv, int64_t G, int64_t seqs, int64_t groups, int64_t q_tokens) {
-    return hkv * (2 * 5 * q_tokens * G + PAGED_ROWS * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * PAGED_ROWS +
+    return hkv * (2 * 9 * q_tokens * G + PAGED_ROWS * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * PAGED_ROWS +
            (int64_t)PAGED_WIDE_CTAS * 256;
 }
 bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_shape &sh) {
@@ -458,18 +462,21 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     const int64_t hkv = a.hkv;
     l.tt_shift = log2_of(rows_tile) - a.g_shift;
     int64_t units = 0, steps = 0, segs = 0;
-    auto level = [&](const PagedLevel &lv) {
+    for (int x = 0; x < 2; ++x) {
+        if (!l.with[x]) continue;
+        const PagedLevel &lv = a.level[x];
         const int64_t tiles = (a.q_tokens >> l.tt_shift) + lv.rows;
+        const int64_t each = (lv.max_length + (1 << l.tile_shift) - 1) >> l.tile_shift;
         units += tiles * hkv;
-        steps += tiles * hkv * ((lv.max_length + (1 << l.tile_shift) - 1) >> l.tile_shift);
+        steps += tiles * hkv * each;
         segs += lv.rows;
-    };
-    for (int x = 0; x < 2; ++x)
-        if (l.with[x]) level(a.level[x]);
+        // What paged_share goes by: prefixes are taken to be of the bound's length, own tokens of half.
+        const double likely = (double)hkv * std::max<int64_t>(a.q_tokens >> l.tt_shift, lv.rows);
+        const double long_each = x == 0 ? (double)each : 0.5 * (each + 1);
+        l.cost += likely * (l.grouped ? long_each * (l.tall ? 2.0 : 1.5) : 1.0 * long_each + 1.6);
+    }
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
     if (steps >= (1LL << 31) || units + l.ctas >= (1LL << 31)) return false;
-    l.steps = (int)steps;
-    l.units = (int)units;
     l.slots = (int)(units + l.ctas);
     auto take = [&](size_t bytes) {
         unsigned char *p = ws + off;
@@ -487,12 +494,12 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
 // is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 64 -> 45 us, 64
 // sequences 86 -> 74); but alone on an SM it takes longer in all, so where its work would fill the
 // GPU for 30 us it follows on all of it (256 sequences: 178 against 201 us side by side).  Costs are
-// the measured us of a step: 0.8 of k_paged alone on an SM, and 1.2 a unit; 1.5 or 2 of k_paged_wide with
-// 128 or 256 rows.
+// the us of a step: 1.0 of k_paged alone on an SM beside k_paged_wide, and 1.6 a unit; 1.5 or 2 of
+// k_paged_wide with 128 or 256 rows.
 void paged_share(PagedLine &wide, PagedLine &own, int sms) {
-    const double w = wide.steps * (wide.tall ? 2.0 : 1.5), o = own.steps * 0.8 + own.units * 1.2;
+    const double w = wide.cost, o = own.cost;
     const int x = (int)(sms * o / (w + o)) + 1;
-    if (x > sms / 2 || o > 30.0 * sms) return;
+    if (x > sms * 3 / 4 || o > 30.0 * sms) return;
     own.ctas = std::min(own.ctas, x);
     wide.ctas = std::min(wide.ctas, sms - x);
 }
@@ -1212,11 +1219,10 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         // Each level by the rows of its segments; the two lines' launches need not wait for one another.
         const int64_t rows_prefix = a.level[0].rows ? paged_rows(q_tokens, a.level[0].rows, sh.q_per_kv) : 0;
         const int64_t rows_own = a.level[1].rows ? paged_rows(q_tokens, a.level[1].rows, sh.q_per_kv) : 0;
-        const auto wide = [](int64_t rows) { return rows > PAGED_WIDE_ROWS; };
-        lines[0].with[0] = rows_prefix > 0 && !wide(rows_prefix);
-        lines[0].with[1] = rows_own > 0 && !wide(rows_own);
-        lines[1].with[0] = wide(rows_prefix);
-        lines[1].with[1] = wide(rows_own);
+        lines[1].with[0] = paged_wide_prefix(rows_prefix);
+        lines[1].with[1] = paged_wide_own(rows_own);
+        lines[0].with[0] = rows_prefix > 0 && !lines[1].with[0];
+        lines[0].with[1] = rows_own > 0 && !lines[1].with[1];
         const bool few = lines[0].with[0] || lines[0].with[1], many = lines[1].with[0] || lines[1].with[1];
         // Tiles of 256 rows where every level has that many: K and V are read half as often.
         const bool tall = (!lines[1].with[0] || rows_prefix > 128) && (!lines[1].with[1] || rows_own > 128);
