@@ -14,8 +14,8 @@
 // transposed).  At a unit's end the four warps' states are joined in the step's own shared memory,
 // which nothing reads any more, and written as one partial.
 //
-// k_paged_merge: a warp per query token and head joins the partials of its prefix and its own
-// pages, and the caller's prior state, in a fixed order.
+// k_paged_merge: a warp, or with few rows four, per query token and head joins the partials of its
+// prefix and its own pages, and the caller's prior state, in a fixed order.
 #include <math.h>
 
 #include <algorithm>
@@ -432,12 +432,14 @@ __device__ __forceinline__ int last_at_most(const int32_t *start, int n, int x) 
 constexpr int PM_NT = 128;
 constexpr int PM_FIRST = 1024;  // blocks that are there before the partials are
 
-template <typename T, int D>
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLines lines) {
     constexpr int V = D / 32;  // channels a lane holds
     const int lane = threadIdx.x & 31;
     const int hq = a.hkv << a.g_shift;
-    const long long row = (long long)blockIdx.x * (PM_NT / 32) + (threadIdx.x >> 5);
+    __shared__ float states[PM_NT / 32][D + 2];
+    const int warp = threadIdx.x >> 5, wi = warp % WPR;  // of the row's warps
+    const long long row = (long long)blockIdx.x * (PM_NT / 32 / WPR) + warp / WPR;
     if (row >= (long long)a.q_tokens * hq) return;
     const int t = (int)(row / hq), hh = (int)(row - (long long)t * hq), head = hh >> a.g_shift, g = hh - (head << a.g_shift);
     // The first blocks twice: once for the instructions, while the partials are still being made (what
@@ -487,8 +489,9 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
         // 32 partials a turn, a lane each: its state, and where its values are.  A partial whose sum is 0
         // summed nothing, and its values are not used.
         const int n = pass ? count[0] + count[1] : min(count[0] + count[1], 32);
+        const int turns = (n + WPR - 1 - wi) / WPR;  // this warp's: every WPR-th
         const int flat = lane * V, quad = (lane * V / 4) * 16 + lane * V % 4;  // this lane's channels in either order
-        float m = prior, z = 0.0f, acc[V];
+        float m = wi == 0 ? prior : -INFINITY, z = 0.0f, acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
         if (m != -INFINITY) {
@@ -497,8 +500,8 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
             for (int i = 0; i < V; ++i) acc[i] = __ldcg(a.prior_o + row * D + flat + i);
         }
 #pragma unroll 1
-        for (int x0 = 0; x0 < n; x0 += 32) {
-            const int x = x0 + lane, v = x < count[0] ? 0 : 1, k = x - (v ? count[0] : 0);
+        for (int x0 = 0; x0 < turns; x0 += 32) {
+            const int x = (x0 + lane) * WPR + wi, v = x < count[0] ? 0 : 1, k = x - (v ? count[0] : 0);
             float2 mine = make_float2(-INFINITY, 0.0f);
             unsigned long long at = 0;
             if (x < n) {
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
             for (int i = 0; i < V; ++i) acc[i] *= f;
             m = mn;
             const unsigned some = __ballot_sync(0xFFFFFFFFu, mine.y != 0.0f);
-            const int c = min(32, n - x0);
+            const int c = min(32, turns - x0);
 #pragma unroll 4
             for (int y = 0; y < c; ++y) {
                 const float wy = __shfl_sync(0xFFFFFFFFu, w, y);
@@ -531,7 +534,34 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
             }
         }
         z = warp_sum(z);
-        if (!pass) continue;
+        if (WPR > 1) {
+            // The row's warps join in shared memory, in their order.
+            if (lane == 0) {
+                states[warp][D] = m;
+                states[warp][D + 1] = z;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) states[warp][flat + i] = acc[i];
+            __syncthreads();
+            float mn = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) mn = fmaxf(mn, states[w][D]);
+            const float ms = mn == -INFINITY ? 0.0f : mn;
+            m = mn;
+            z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) {
+                const float f = exp2_fast(states[w][D] - ms), zw = states[w][D + 1];
+                if (zw == 0.0f) continue;
+                z = fmaf(zw, f, z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(states[w][flat + i], f, acc[i]);
+            }
+            __syncthreads();  // (the next pass writes them again)
+        }
+        if (!pass || wi) continue;
         const float inv = z == 0.0f ? 0.0f : 1.0f / z;
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row * D + lane * V);
 #pragma unroll
@@ -576,10 +606,19 @@ cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorM
 }
 
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLines &lines, int dtype, int d, cudaStream_t s) {
-    const long long rows = (long long)a.q_tokens * (a.hkv << a.g_shift), blocks = (rows + PM_NT / 32 - 1) / (PM_NT / 32);
+    const long long rows = (long long)a.q_tokens * (a.hkv << a.g_shift);
+    // Few rows with many partials each (39 of 128 rows, 128K tokens: 98 -> 91 us a call) have warps to spare.
+    double partials = 0.0;  // of a row, about
+    for (const PagedLine &l : lines.l)
+        if (l.units > 0) partials = std::max(partials, (double)l.ctas / l.units);
+    const int wpr = rows <= 1024 && partials >= 7.0 ? 4 : 1;
+    const long long blocks = (rows * wpr + PM_NT / 32 - 1) / (PM_NT / 32);
     if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-#define VERKV_PM(TT, DT, DD) \
-    if (dtype == DT && d == DD) return launch_pdl(k_paged_merge<TT, DD>, dim3((unsigned)blocks), dim3(PM_NT), 0, s, a, lines);
+#define VERKV_PM(TT, DT, DD)                                                                                               \
+    if (dtype == DT && d == DD) {                                                                                          \
+        if (wpr == 4) return launch_pdl(k_paged_merge<TT, DD, 4>, dim3((unsigned)blocks), dim3(PM_NT), 0, s, a, lines);    \
+        return launch_pdl(k_paged_merge<TT, DD, 1>, dim3((unsigned)blocks), dim3(PM_NT), 0, s, a, lines);                  \
+    }
     VERKV_PM(PgBf16, VERKV_BF16, 128) VERKV_PM(PgBf16, VERKV_BF16, 64)
     VERKV_PM(PgF16, VERKV_F16, 128) VERKV_PM(PgF16, VERKV_F16, 64)
 #undef VERKV_PM

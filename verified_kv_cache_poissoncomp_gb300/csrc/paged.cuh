@@ -57,7 +57,7 @@ struct PagedLine {
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
     int tall;                   // (host: tiles of 256 rows)
-    double cost;                // (host: us of one SM)
+    double cost, units;         // (host: us of one SM; about how many units)
     int2 *rec;                  // {per, 0}, then {work before, units before} of each segment with work; per 0: a bad segment, no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
     float *part_o;

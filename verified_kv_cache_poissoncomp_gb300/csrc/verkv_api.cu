@@ -473,6 +473,7 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
         // What paged_share goes by: prefixes are taken to be of the bound's length, own tokens of half.
         const double likely = (double)hkv * std::max<int64_t>(a.q_tokens >> l.tt_shift, lv.rows);
         const double long_each = x == 0 ? (double)each : 0.5 * (each + 1);
+        l.units += likely;
         l.cost += likely * (l.grouped ? long_each * (l.tall ? 2.0 : 1.5) : 1.0 * long_each + 1.6);
     }
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
