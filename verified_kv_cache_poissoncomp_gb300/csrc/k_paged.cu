@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
 #pragma unroll 1
         for (int dry = 1; dry >= 0; --dry) {
             if (!dry) {
-                // (k_paged_wide lets this kernel start when it has waited itself)
+                // (the other kernel of the call lets this one start when it has waited itself)
                 if (wait_first) pdl_wait();
                 pdl_trigger();
             }

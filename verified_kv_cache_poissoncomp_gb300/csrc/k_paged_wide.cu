@@ -112,7 +112,8 @@ __device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_fl
 
 template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(PW_NT, 1)
-    k_paged_wide(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const __grid_constant__ CUtensorMap map) {
+    k_paged_wide(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int wait_first,
+                 const __grid_constant__ CUtensorMap map) {
     using LY = WideLayout<D, TILES>;
     using W = Weights<T>;
     constexpr int NS = LY::NS, R = LY::R;
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
 #pragma unroll 1
         for (int dry = 1; dry >= 0; --dry) {
             if (!dry) {
-                pdl_wait();
+                if (wait_first) pdl_wait();
                 pdl_trigger();
             }
             // (the chains' states have no use for their place yet)
@@ -557,11 +558,13 @@ __global__ void __launch_bounds__(PW_NT, 1)
     __syncthreads();
     tcgen05_after_sync();
     if (warp == PW_MMA) tmem_free(tm, 512);
+    pdl_wait();  // the launch before this one is done when this one is
 }
 
 }  // namespace
 
-cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const CUtensorMap &map, int dtype, int d, cudaStream_t s) {
+cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype,
+                              int d, cudaStream_t s) {
     PagedArgs a = args;
     // a scale that rounds to 0 would make the masked logits' -infinity not a number
     if (fabsf(a.scale_log2) < FLT_MIN) a.scale_log2 = copysignf(FLT_MIN, a.scale_log2);
@@ -571,7 +574,7 @@ cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const C
         const size_t smem = WideLayout<DD, NN>::BYTES;                                          \
         const cudaError_t e = ensure_smem((const void *)k_paged_wide<TT, DD, NN>, smem);        \
         if (e != cudaSuccess) return e;                                                         \
-        return launch_pdl(k_paged_wide<TT, DD, NN>, dim3(l.ctas), dim3(PW_NT), smem, s, a, l, map); \
+        return launch_pdl(k_paged_wide<TT, DD, NN>, dim3(l.ctas), dim3(PW_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
     }
     VERKV_WIDE(PgBf16, VERKV_BF16, 128, 1) VERKV_WIDE(PgBf16, VERKV_BF16, 128, 2)
     VERKV_WIDE(PgBf16, VERKV_BF16, 64, 1) VERKV_WIDE(PgBf16, VERKV_BF16, 64, 2)

@@ -85,11 +85,12 @@ constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
 constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
 
 cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long long rows, int d, int box_rows);
-// wait_first false: the launch before it on the stream is this call's k_paged_wide, which it need not
+// wait_first false: the launch before it on the stream is this call's other kernel, which it need not
 // wait for to begin.
 cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype, int d,
                          cudaStream_t s);
-cudaError_t launch_paged_wide(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, int dtype, int d, cudaStream_t s);
+cudaError_t launch_paged_wide(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype,
+                              int d, cudaStream_t s);
 struct PagedLines {
     PagedLine l[PAGED_LINES];
 };

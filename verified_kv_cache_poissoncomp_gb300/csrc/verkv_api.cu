@@ -497,12 +497,13 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
 // GPU for 30 us it follows on all of it (256 sequences: 178 against 201 us side by side).  Costs are
 // the us of a step: 1.0 of k_paged alone on an SM beside k_paged_wide, and 1.6 a unit; 1.5 or 2 of
 // k_paged_wide with 128 or 256 rows.
-void paged_share(PagedLine &wide, PagedLine &own, int sms) {
+bool paged_share(PagedLine &wide, PagedLine &own, int sms) {
     const double w = wide.cost, o = own.cost;
     const int x = (int)(sms * o / (w + o)) + 1;
-    if (x > sms * 3 / 4 || o > 30.0 * sms) return;
+    if (x > sms * 3 / 4 || o > 30.0 * sms) return false;
     own.ctas = std::min(own.ctas, x);
     wide.ctas = std::min(wide.ctas, sms - x);
+    return true;
 }
 
 }  // namespace
@@ -1242,18 +1243,18 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
             return paged_tensor_map(&map, pages->kv, pages->dtype, (long long)pages->num_pages * a.hkv * pages->page_tokens,
                                     sh.head_dim, std::min(pages->page_tokens, tile));
         };
-        if (few && many) paged_share(lines[1], lines[0], ctx->sms);
-        if (many) {
-            VERKV_CUDA(make_map(PAGED_WIDE_TILE), "tensor map of the pages");
-            VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_WIDE, ctx->main, [&] {
-                           return launch_paged_wide(a, lines[1], map, pages->dtype, sh.head_dim, ctx->main);
-                       }), "k_paged_wide");
-        }
-        if (few) {
-            VERKV_CUDA(make_map(PAGED_TILE), "tensor map of the pages");
-            VERKV_CUDA(tracked(ctx, VERKV_K_PAGED, ctx->main, [&] {
-                           return launch_paged(a, lines[0], map, !many || ctx->prof_on, pages->dtype, sh.head_dim, ctx->main);
-                       }), "k_paged");
+        // Side by side, the longer one begins first; one after the other, k_paged, whose start is the longer
+        // one with many sequences, begins while the kernel ahead of the call still runs.
+        const bool beside = few && many && paged_share(lines[1], lines[0], ctx->sms);
+        for (int turn = 0; turn < 2; ++turn) {
+            const bool wide = (turn == 0) == (beside || !few);
+            if (!(wide ? many : few)) continue;
+            const bool wait_first = turn == 0 || !few || !many || ctx->prof_on;
+            VERKV_CUDA(make_map(wide ? PAGED_WIDE_TILE : PAGED_TILE), "tensor map of the pages");
+            VERKV_CUDA(tracked(ctx, wide ? VERKV_K_PAGED_WIDE : VERKV_K_PAGED, ctx->main, [&] {
+                           return wide ? launch_paged_wide(a, lines[1], map, wait_first, pages->dtype, sh.head_dim, ctx->main)
+                                       : launch_paged(a, lines[0], map, wait_first, pages->dtype, sh.head_dim, ctx->main);
+                       }), wide ? "k_paged_wide" : "k_paged");
         }
     }
     VERKV_CUDA(tracked(ctx, VERKV_K_PAGED_MERGE, ctx->main, [&] { return launch_paged_merge(a, both, pages->dtype, sh.head_dim, ctx->main); }), "k_paged_merge");
