@@ -110,18 +110,11 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
         const int box = min(1 << a.page_shift, PAGED_TILE);  // tokens of a page in one step
         PagedWalk wk;
-        // Once for its instructions, while the kernel before this one still runs; what it reads may
-        // change until the wait, and is not used.
-#pragma unroll 1
-        for (int dry = 1; dry >= 0; --dry) {
-            if (!dry) {
-                // (the other kernel of the call lets this one start when it has waited itself)
-                if (wait_first) pdl_wait();
-                pdl_trigger();
-            }
-            // (the queries' place holds nothing yet)
-            wk.start(a, l, blockIdx.x, dry != 0, reinterpret_cast<int2 *>(pg_smem + LY::Q), LY::QN * R * LY::QROW / 8);
-        }
+        // (the other kernel of the call lets this one start when it has waited itself)
+        if (wait_first) pdl_wait();
+        pdl_trigger();
+        // (the queries' place holds nothing yet)
+        wk.start(a, l, blockIdx.x, reinterpret_cast<int2 *>(pg_smem + LY::Q), LY::QN * R * LY::QROW / 8);
         // The walk is one piece ahead of the copies, so that a piece's page ids are there when its
         // first step is.
         auto fetch = [&](Piece &p) -> bool {
@@ -233,25 +226,18 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
             ++joins;
             return __all_sync(0xFFFFFFFFu, ok);
         };
-        // Round -1 runs a step over whatever the first slot holds, for its instructions: a kernel starts
-        // with cold instruction caches, and they would else be fetched when the first step has arrived
-        // instead of while it is on its way.  (No copy has been started into V's part of a slot that the
-        // round could write: valid is 64.)
-        for (int j = -1;; ++j) {
-            const int k = j < 0 ? 0 : j % NS;
-            StepDesc s = {PG_FIRST, PAGED_TILE, 0, R, 0, 0, 0, -1};
-            if (j >= 0) {
-                const bool ok = mbar_wait_or_abort(&full[k], (uint32_t)((j / NS) & 1), abort);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    if (lane == 0) {
-                        *abort = 1;
-                        raise_error(a.err, ERR_TIMEOUT);
-                    }
-                    break;
+        for (int j = 0;; ++j) {
+            const int k = j % NS;
+            const bool ok = mbar_wait_or_abort(&full[k], (uint32_t)((j / NS) & 1), abort);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                if (lane == 0) {
+                    *abort = 1;
+                    raise_error(a.err, ERR_TIMEOUT);
                 }
-                s = desc[k];
-                if (s.flags & PG_END) break;
+                break;
             }
+            const StepDesc s = desc[k];
+            if (s.flags & PG_END) break;
             unsigned char *st = pg_smem + (size_t)k * LY::STAGE;
             if (s.flags & PG_FIRST) {
                 const uint32_t qb = smem_addr(pg_smem + LY::Q) + (s.q * R + rb + (mi & 1) * 8 + ri) * LY::QROW + (mi >> 1) * 16;
@@ -359,8 +345,6 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                     }
                 }
             }
-            if (j < 0) continue;
-
             if (s.flags & PG_LAST) {
                 // Join the four warps' states: each scales its sums to the common maximum and lays
                 // them in the slot, and all threads add the four and write the partial.
@@ -423,14 +407,13 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
 __device__ __forceinline__ int last_at_most(const int32_t *start, int n, int x) {
     int c = 0;
 #pragma unroll 4
-    for (int i = threadIdx.x & 31; i <= n; i += 32) c += __ldcg(start + i) <= x ? 1 : 0;
+    for (int i = threadIdx.x & 31; i <= n; i += 32) c += start[i] <= x ? 1 : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
     return c - 1;
 }
 
 constexpr int PM_NT = 128;
-constexpr int PM_FIRST = 1024;  // blocks that are there before the partials are
 
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLines lines) {
@@ -438,136 +421,127 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
     const int lane = threadIdx.x & 31;
     const int hq = a.hkv << a.g_shift;
     __shared__ float states[PM_NT / 32][D + 2];
+    pdl_wait();
+    pdl_trigger();
     const int warp = threadIdx.x >> 5, wi = warp % WPR;  // of the row's warps
     const long long row = (long long)blockIdx.x * (PM_NT / 32 / WPR) + warp / WPR;
     if (row >= (long long)a.q_tokens * hq) return;
     const int t = (int)(row / hq), hh = (int)(row - (long long)t * hq), head = hh >> a.g_shift, g = hh - (head << a.g_shift);
-    // The first blocks twice: once for the instructions, while the partials are still being made (what
-    // it reads then may change and is not used, and every index is within its buffer whatever the
-    // records hold).
-#pragma unroll 1
-    for (int pass = blockIdx.x < PM_FIRST ? 0 : 1; pass < 2; ++pass) {
-        if (pass) {
-            pdl_wait();
-            pdl_trigger();
-        }
-        const int s = a.q_start ? last_at_most(a.q_start, a.seqs, t) : t;
+    const int s = a.q_start ? last_at_most(a.q_start, a.seqs, t) : t;
 
-        // Where the row's partials are: of its prefix, then of its own pages.
-        const float *po[2] = {}, *pm[2] = {};
-        int count[2] = {0, 0}, rows[2] = {0, 0};  // a slot's rows
-        bool grouped[2] = {false, false};
+    // Where the row's partials are: of its prefix, then of its own pages.
+    const float *po[2] = {}, *pm[2] = {};
+    int count[2] = {0, 0}, rows[2] = {0, 0};  // a slot's rows
+    bool grouped[2] = {false, false};
 #pragma unroll
-        for (int own = 0; own < 2; ++own) {
-            const int at = lines.l[1].with[own] ? 1 : 0;
-            const PagedLine &l = lines.l[at];
-            if (!l.with[own]) continue;
-            const int r = own ? s : a.group_start ? last_at_most(a.group_start, a.level[0].rows, s) : 0;
-            if (r < 0 || r >= a.level[own].rows) continue;
-            const int i = r + (own && l.with[0] ? a.level[0].rows : 0);
-            const int per = __ldcg(l.rec).x;
-            const int2 before = __ldcg(l.rec + 1 + i);
-            bool bad = false;
-            const PagedSeg sg = paged_segment(a, l, i, bad);
-            const int j = t - sg.q0;
-            if (j < 0 || j >= sg.qn || per <= 0) continue;  // (per 0: a bad segment, nothing was done)
-            const int mt = j >> l.tt_shift, steps = paged_steps(sg, l, mt);
-            if (steps == 0) continue;
-            const int w0 = before.x + paged_steps_before(sg, l, mt) * a.hkv + head * steps;
-            const int c0 = (unsigned)w0 / (unsigned)per, c1 = (unsigned)(w0 + steps - 1) / (unsigned)per;
-            const int in = ((j - (mt << l.tt_shift)) << a.g_shift) + g;
-            const int slot = clampi(c0 + before.y + mt * a.hkv + head, 0, l.slots - 1);
-            count[own] = clampi(c1 - c0 + 1, 0, l.slots - slot);
-            rows[own] = 1 << (l.tt_shift + a.g_shift);
-            grouped[own] = l.grouped != 0;
-            po[own] = l.part_o + (long long)slot * rows[own] * D + (l.grouped ? (in >> 2) * (D * 4) + (in & 3) * 4 : in * D);
-            pm[own] = l.part_ml + ((long long)slot * rows[own] + in) * 2;
-        }
-        float prior = -INFINITY;
-        if (a.prior_lse) prior = __ldcg(a.prior_lse + row) * 1.4426950408889634f;
+    for (int own = 0; own < 2; ++own) {
+        const int at = lines.l[1].with[own] ? 1 : 0;
+        const PagedLine &l = lines.l[at];
+        if (!l.with[own]) continue;
+        const int r = own ? s : a.group_start ? last_at_most(a.group_start, a.level[0].rows, s) : 0;
+        if (r < 0 || r >= a.level[own].rows) continue;
+        const int i = r + (own && l.with[0] ? a.level[0].rows : 0);
+        const int per = l.rec[0].x;
+        const int2 before = l.rec[1 + i];
+        bool bad = false;
+        const PagedSeg sg = paged_segment(a, l, i, bad);
+        const int j = t - sg.q0;
+        if (j < 0 || j >= sg.qn || per <= 0) continue;  // (per 0: a bad segment, nothing was done)
+        const int mt = j >> l.tt_shift, steps = paged_steps(sg, l, mt);
+        if (steps == 0) continue;
+        const int w0 = before.x + paged_steps_before(sg, l, mt) * a.hkv + head * steps;
+        const int c0 = (unsigned)w0 / (unsigned)per, c1 = (unsigned)(w0 + steps - 1) / (unsigned)per;
+        const int in = ((j - (mt << l.tt_shift)) << a.g_shift) + g;
+        const int slot = clampi(c0 + before.y + mt * a.hkv + head, 0, l.slots - 1);
+        count[own] = clampi(c1 - c0 + 1, 0, l.slots - slot);
+        rows[own] = 1 << (l.tt_shift + a.g_shift);
+        grouped[own] = l.grouped != 0;
+        po[own] = l.part_o + (long long)slot * rows[own] * D + (l.grouped ? (in >> 2) * (D * 4) + (in & 3) * 4 : in * D);
+        pm[own] = l.part_ml + ((long long)slot * rows[own] + in) * 2;
+    }
+    float prior = -INFINITY;
+    if (a.prior_lse) prior = a.prior_lse[row] * 1.4426950408889634f;
 
-        // 32 partials a turn, a lane each: its state, and where its values are.  A partial whose sum is 0
-        // summed nothing, and its values are not used.
-        const int n = pass ? count[0] + count[1] : min(count[0] + count[1], 32);
-        const int turns = (n + WPR - 1 - wi) / WPR;  // this warp's: every WPR-th
-        const int flat = lane * V, quad = (lane * V / 4) * 16 + lane * V % 4;  // this lane's channels in either order
-        float m = wi == 0 ? prior : -INFINITY, z = 0.0f, acc[V];
+    // 32 partials a turn, a lane each: its state, and where its values are.  A partial whose sum is 0
+    // summed nothing, and its values are not used.
+    const int n = count[0] + count[1];
+    const int turns = (n + WPR - 1 - wi) / WPR;  // this warp's: every WPR-th
+    const int flat = lane * V, quad = (lane * V / 4) * 16 + lane * V % 4;  // this lane's channels in either order
+    float m = wi == 0 ? prior : -INFINITY, z = 0.0f, acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    if (m != -INFINITY) {
+        z = lane == 0 ? 1.0f : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = a.prior_o[row * D + flat + i];
+    }
+#pragma unroll 1
+    for (int x0 = 0; x0 < turns; x0 += 32) {
+        const int x = (x0 + lane) * WPR + wi, v = x < count[0] ? 0 : 1, k = x - (v ? count[0] : 0);
+        float2 mine = make_float2(-INFINITY, 0.0f);
+        unsigned long long at = 0;
+        if (x < n) {
+            mine = *reinterpret_cast<const float2 *>((v ? pm[1] : pm[0]) + (long long)k * (v ? rows[1] : rows[0]) * 2);
+            at = reinterpret_cast<unsigned long long>((v ? po[1] : po[0]) + (long long)k * (v ? rows[1] : rows[0]) * D);
+        }
+        const unsigned in_quads = __ballot_sync(0xFFFFFFFFu, v ? grouped[1] : grouped[0]);
+        const float mn = fmaxf(m, warp_max(mine.x)), ms = mn == -INFINITY ? 0.0f : mn;
+        const float f = exp2_fast(m - ms), w = exp2_fast(mine.x - ms);
+        z = z * f + (mine.y == 0.0f ? 0.0f : mine.y * w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= f;
+        m = mn;
+        const unsigned some = __ballot_sync(0xFFFFFFFFu, mine.y != 0.0f);
+        const int c = min(32, turns - x0);
+#pragma unroll 4
+        for (int y = 0; y < c; ++y) {
+            const float wy = __shfl_sync(0xFFFFFFFFu, w, y);
+            const float *src = reinterpret_cast<const float *>(__shfl_sync(0xFFFFFFFFu, at, y)) + ((in_quads >> y & 1) ? quad : flat);
+            float u[V];
+            if (V == 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(src);
+                u[0] = q.x; u[1] = q.y; u[V - 2] = q.z; u[V - 1] = q.w;
+            } else {
+                const float2 q = *reinterpret_cast<const float2 *>(src);
+                u[0] = q.x; u[1] = q.y;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = (some >> y & 1) ? fmaf(u[i], wy, acc[i]) : acc[i];
+        }
+    }
+    z = warp_sum(z);
+    if (WPR > 1) {
+        // The row's warps join in shared memory, in their order.
+        if (lane == 0) {
+            states[warp][D] = m;
+            states[warp][D + 1] = z;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) states[warp][flat + i] = acc[i];
+        __syncthreads();
+        float mn = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) mn = fmaxf(mn, states[w][D]);
+        const float ms = mn == -INFINITY ? 0.0f : mn;
+        m = mn;
+        z = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-        if (m != -INFINITY) {
-            z = lane == 0 ? 1.0f : 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = __ldcg(a.prior_o + row * D + flat + i);
+        for (int w = 0; w < WPR; ++w) {
+            const float f = exp2_fast(states[w][D] - ms), zw = states[w][D + 1];
+            if (zw == 0.0f) continue;
+            z = fmaf(zw, f, z);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(states[w][flat + i], f, acc[i]);
         }
-#pragma unroll 1
-        for (int x0 = 0; x0 < turns; x0 += 32) {
-            const int x = (x0 + lane) * WPR + wi, v = x < count[0] ? 0 : 1, k = x - (v ? count[0] : 0);
-            float2 mine = make_float2(-INFINITY, 0.0f);
-            unsigned long long at = 0;
-            if (x < n) {
-                mine = __ldcg(reinterpret_cast<const float2 *>((v ? pm[1] : pm[0]) + (long long)k * (v ? rows[1] : rows[0]) * 2));
-                at = reinterpret_cast<unsigned long long>((v ? po[1] : po[0]) + (long long)k * (v ? rows[1] : rows[0]) * D);
-            }
-            const unsigned in_quads = __ballot_sync(0xFFFFFFFFu, v ? grouped[1] : grouped[0]);
-            const float mn = fmaxf(m, warp_max(mine.x)), ms = mn == -INFINITY ? 0.0f : mn;
-            const float f = exp2_fast(m - ms), w = exp2_fast(mine.x - ms);
-            z = z * f + (mine.y == 0.0f ? 0.0f : mine.y * w);
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] *= f;
-            m = mn;
-            const unsigned some = __ballot_sync(0xFFFFFFFFu, mine.y != 0.0f);
-            const int c = min(32, turns - x0);
-#pragma unroll 4
-            for (int y = 0; y < c; ++y) {
-                const float wy = __shfl_sync(0xFFFFFFFFu, w, y);
-                const float *src = reinterpret_cast<const float *>(__shfl_sync(0xFFFFFFFFu, at, y)) + ((in_quads >> y & 1) ? quad : flat);
-                float u[V];
-                if (V == 4) {
-                    const float4 q = __ldcg(reinterpret_cast<const float4 *>(src));
-                    u[0] = q.x; u[1] = q.y; u[V - 2] = q.z; u[V - 1] = q.w;
-                } else {
-                    const float2 q = __ldcg(reinterpret_cast<const float2 *>(src));
-                    u[0] = q.x; u[1] = q.y;
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = (some >> y & 1) ? fmaf(u[i], wy, acc[i]) : acc[i];
-            }
-        }
-        z = warp_sum(z);
-        if (WPR > 1) {
-            // The row's warps join in shared memory, in their order.
-            if (lane == 0) {
-                states[warp][D] = m;
-                states[warp][D + 1] = z;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) states[warp][flat + i] = acc[i];
-            __syncthreads();
-            float mn = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < WPR; ++w) mn = fmaxf(mn, states[w][D]);
-            const float ms = mn == -INFINITY ? 0.0f : mn;
-            m = mn;
-            z = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WPR; ++w) {
-                const float f = exp2_fast(states[w][D] - ms), zw = states[w][D + 1];
-                if (zw == 0.0f) continue;
-                z = fmaf(zw, f, z);
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(states[w][flat + i], f, acc[i]);
-            }
-            __syncthreads();  // (the next pass writes them again)
-        }
-        if (!pass || wi) continue;
-        const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row * D + lane * V);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) dst[i] = T::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-        if (a.lse && lane == 0) a.lse[row] = z == 0.0f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
     }
+    if (wi) return;
+    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row * D + lane * V);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) dst[i] = T::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = z == 0.0f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
 }
 
 }  // namespace

@@ -166,19 +166,12 @@ __global__ void __launch_bounds__(PW_NT, 1)
 
     if (warp == PW_COPY) {
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
-        // Nothing of the caller's is read before the kernel ahead is done -- but for the walk, once, for
-        // its instructions; what it reads may change until the wait, and is not used.  The other warps
-        // touch the caller's data only after the first piece that this one announces.
+        // The other warps touch the caller's data only after the first piece that this one announces.
+        if (wait_first) pdl_wait();
+        pdl_trigger();
+        // (the chains' states have no use for their place yet)
         PagedWalk wk;
-#pragma unroll 1
-        for (int dry = 1; dry >= 0; --dry) {
-            if (!dry) {
-                if (wait_first) pdl_wait();
-                pdl_trigger();
-            }
-            // (the chains' states have no use for their place yet)
-            wk.start(a, l, blockIdx.x, dry != 0, reinterpret_cast<int2 *>(ml), 2 * 128);
-        }
+        wk.start(a, l, blockIdx.x, reinterpret_cast<int2 *>(ml), 2 * 128);
         const int box = min(1 << a.page_shift, PAGED_WIDE_TILE);
         int j = 0, np = 0;  // slots and pieces so far
         bool go = true;
@@ -206,7 +199,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                         const int p = p0 + lane;
                         int id = 0;
                         if (p <= (vis - 1) >> a.page_shift) {
-                            id = __ldcg(row + p);
+                            id = row[p];
                             if (id < 0 || id >= a.num_pages) {
                                 raise_error(a.err, ERR_PAGE);
                                 id = 0;
@@ -385,24 +378,16 @@ __global__ void __launch_bounds__(PW_NT, 1)
         const float c = fabsf(a.scale_log2);
         const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // a negative scale turns Q round
         uint32_t ns = 0;
-        PieceDesc pd = {};
-        // Round -1 runs the softmax once over whatever tensor memory holds, for its instructions: a
-        // kernel starts with cold instruction caches, and these 10 KB would else be fetched (5 us) when
-        // the first product is ready instead of while its operands are on their way.  No product is
-        // in flight then: the first waits for this warp's Q.
-        for (int np = -1;; ++np) {
-            const bool dry = np < 0;
-            bool real = true, busy = true;
-            int lim = 0, count = 1;
-            if (!dry) {
-                if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
-                pd = pieces[np % PW_PIECES];
-                if (pd.steps == 0) break;
-                const int jj = row >> a.g_shift, hh = row - (jj << a.g_shift);
-                real = jj < pd.nq;
-                busy = __any_sync(0xFFFFFFFFu, real);  // a warp without rows only keeps step
-                lim = real ? pd.lim0 + pd.limd * jj : 0;
-                count = TILES == 2 ? pd.steps : (pd.steps + 1 - i) / 2;
+        for (int np = 0;; ++np) {
+            if (!wait(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
+            const PieceDesc pd = pieces[np % PW_PIECES];
+            if (pd.steps == 0) break;
+            const int jj = row >> a.g_shift, hh = row - (jj << a.g_shift);
+            const bool real = jj < pd.nq;
+            const bool busy = __any_sync(0xFFFFFFFFu, real);  // a warp without rows only keeps step
+            const int lim = real ? pd.lim0 + pd.limd * jj : 0;
+            const int count = TILES == 2 ? pd.steps : (pd.steps + 1 - i) / 2;
+            {
                 // Q, swizzled as the copies are: a thread a row; with one tile the chains halve it.
                 const uint16_t *src = a.q + (long long)(pd.q0 + (real ? jj : 0)) * a.q_ts + (long long)((pd.head << a.g_shift) + hh) * a.q_hs;
                 unsigned char *dst = pw_smem + LY::Q + (TILES == 2 ? i * LY::SLOT : 0);
@@ -425,7 +410,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
             bool ok = true;
 #pragma unroll 1
             for (int n = 0; n < count; ++n) {
-                if (!dry && !(ok = wait(&s_full[i], ns))) break;
+                if (!(ok = wait(&s_full[i], ns))) break;
                 tcgen05_after_sync();
                 if (busy) {
                     uint32_t s[128];
@@ -474,7 +459,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                         }
                         tmem_st32(ts + 32 * h, p);
                         tmem_wait_st();
-                        if (h == 0 && !dry) {
+                        if (h == 0) {
                             tcgen05_before_sync();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&h_full[i]);
@@ -482,7 +467,6 @@ __global__ void __launch_bounds__(PW_NT, 1)
                     }
                     sum += (lo2(part[0]) + hi2(part[0])) + (lo2(part[1]) + hi2(part[1]));
                 }
-                if (dry) break;
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0) {
@@ -491,7 +475,6 @@ __global__ void __launch_bounds__(PW_NT, 1)
                 }
                 ++ns;
             }
-            if (dry) continue;
             if (!ok) break;
             if (TILES == 1) {
                 // Each chain tells the other its rows' reference and sum.

@@ -77,8 +77,8 @@ struct PagedArgs {
     float *lse;
 };
 
-constexpr int PAGED_MAX_CTAS = 512;   // of k_paged
-constexpr int PAGED_WIDE_CTAS = 256;  // of k_paged_wide
+constexpr int PAGED_MAX_CTAS = 304;   // of k_paged: two an SM
+constexpr int PAGED_WIDE_CTAS = 152;  // of k_paged_wide
 constexpr int PAGED_TILE = 64;        // tokens of a step of k_paged
 constexpr int PAGED_ROWS = 32;        // most rows of its units (16 or 32)
 constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
@@ -109,9 +109,6 @@ __device__ __forceinline__ int paged_segments(const PagedArgs &a, const PagedLin
     return (l.with[0] ? a.level[0].rows : 0) + (l.with[1] ? a.level[1].rows : 0);
 }
 
-// Loads that may happen before the kernel ahead is done (see PagedWalk::start, k_paged_merge) go past
-// the L1 cache, which would give the same old value again after the wait.
-//
 // Segment i.  Everything read from the device is clamped to its range, so that no later index
 // leaves the tensors; `bad` is set where that changed something.
 __device__ __forceinline__ PagedSeg paged_segment(const PagedArgs &a, const PagedLine &l, int i, bool &bad) {
@@ -121,20 +118,20 @@ __device__ __forceinline__ PagedSeg paged_segment(const PagedArgs &a, const Page
     s.row = s.own ? i - np : i;
     int s0 = s.row, s1 = s.row + 1;
     if (!s.own) {
-        const int r0 = a.group_start ? __ldcg(a.group_start + s.row) : 0;
-        const int r1 = a.group_start ? __ldcg(a.group_start + s.row + 1) : a.seqs;
+        const int r0 = a.group_start ? a.group_start[s.row] : 0;
+        const int r1 = a.group_start ? a.group_start[s.row + 1] : a.seqs;
         s0 = clampi(r0, 0, a.seqs);
         s1 = clampi(r1, s0, a.seqs);
         bad |= s0 != r0 || s1 != r1 || (s.row == 0 && r0 != 0) || (s.row == np - 1 && r1 != a.seqs);
     }
-    const int r0 = a.q_start ? __ldcg(a.q_start + s0) : s0;
-    const int r1 = a.q_start ? __ldcg(a.q_start + s1) : s1;
+    const int r0 = a.q_start ? a.q_start[s0] : s0;
+    const int r1 = a.q_start ? a.q_start[s1] : s1;
     s.q0 = clampi(r0, 0, a.q_tokens);
     const int q1 = clampi(r1, s.q0, a.q_tokens);
     bad |= s.q0 != r0 || q1 != r1 || (s0 == 0 && s.q0 != 0) || (s1 == a.seqs && q1 != a.q_tokens);
     s.qn = q1 - s.q0;
     const PagedLevel &lv = a.level[s.own ? 1 : 0];
-    const int len = __ldcg(lv.length + s.row);
+    const int len = lv.length[s.row];
     s.len = clampi(len, 0, lv.max_length);
     bad |= s.len != len;
     return s;
@@ -182,9 +179,9 @@ struct PagedWalk {
     }
 
     // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also writes
-    // how long a run is and reports bad segments, unless `dry`.  First the whole
+    // how long a run is and reports bad segments.  First the whole
     // line's steps, keeping each segment's in shared memory (`cap` of them) as it goes, then the place.
-    __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c, bool dry, int2 *cache, int cap) {
+    __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c, int2 *cache, int cap) {
         const int lane = threadIdx.x & 31;
         n = paged_segments(a, l);
         seg = n;
@@ -201,7 +198,7 @@ struct PagedWalk {
         total = __reduce_add_sync(0xFFFFFFFFu, total) * a.hkv;
         bad = __any_sync(0xFFFFFFFFu, bad);
         const int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
-        if (c == 0 && !dry && lane == 0) {
+        if (c == 0 && lane == 0) {
             l.rec[0] = make_int2(per, 0);
             if (bad) raise_error(a.err, ERR_PAGE);
         }
