@@ -14,6 +14,11 @@
 // the order S(0) S(1) | P V(0) S(2) | P V(1) S(3) | ..., in which the tensor core executes them, so
 // that S(n + 2) may overwrite the P that P V(n) reads.
 //
+// One warp issues all products, an elected lane of it, in step: its descriptors and barriers stay in
+// uniform registers, and a step's 32 instructions are issued while the tensor core works.  (Issued by
+// a thread in a branch of its own, 256 sequences behind 32K tokens took 178 us a call instead of 158;
+// two such threads, one a chain, taking turns at a barrier: 157, and 8 % more with few queries.)
+//
 // Warps: 0-3 and 4-7 hold the rows of the chains, a thread a row (no shuffles); 8 issues the
 // products; 9 walks the line and copies.  The reference `ref` of a row's weights is its running
 // maximum less SHIFT, and is raised -- with O scaled in tensor memory -- only when the maximum has
@@ -33,8 +38,8 @@ namespace verkv {
 
 namespace {
 
-constexpr int PW_NT = 352;
-constexpr int PW_MMA = 8, PW_COPY = 10;  // warps (8 and 9: a chain's products each)
+constexpr int PW_NT = 320;
+constexpr int PW_MMA = 8, PW_COPY = 9;  // warps
 constexpr int PW_PIECES = 8;            // ring of pieces: the copies are at most a ring of slots ahead
 
 struct PieceDesc {
@@ -59,8 +64,8 @@ struct WideLayout {
     static constexpr int ML = RING + NS * SLOT;                          // float [2][128][2]
     static constexpr int PIECES = ML + 2 * 128 * 2 * 4;                  // PieceDesc [PW_PIECES]
     static constexpr int BARS = (PIECES + PW_PIECES * (int)sizeof(PieceDesc) + 7) / 8 * 8;
-    // full, empty [NS]; piece [PW_PIECES]; s_full, h_full, p_full [2]; q_full, o_full, ml_full; drain, turn [2]
-    static constexpr int NBARS = 2 * NS + PW_PIECES + 6 + 7;
+    // full, empty [NS]; piece [PW_PIECES]; s_full, h_full, p_full [2]; q_full, o_full, ml_full, drain
+    static constexpr int NBARS = 2 * NS + PW_PIECES + 6 + 4;
     static constexpr int BYTES = BARS + NBARS * 8 + 16;
 };
 
@@ -120,8 +125,8 @@ __global__ void __launch_bounds__(PW_NT, 1)
     extern __shared__ __align__(1024) unsigned char pw_smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(pw_smem + LY::BARS), *empty = full + NS, *piece = empty + NS;
     uint64_t *s_full = piece + PW_PIECES, *h_full = s_full + 2, *p_full = h_full + 2, *q_full = p_full + 2, *o_full = q_full + 1;
-    uint64_t *ml_full = o_full + 1, *drain = ml_full + 1, *turn = drain + 2;
-    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(turn + 2);
+    uint64_t *ml_full = o_full + 1, *drain = ml_full + 1;
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_at + 1);
     PieceDesc *pieces = reinterpret_cast<PieceDesc *>(pw_smem + LY::PIECES);
     float *ml = reinterpret_cast<float *>(pw_smem + LY::ML);
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     if (tid == 0) {
         for (int k = 0; k < NS; ++k) {
             mbar_init(&full[k], 1);
-            mbar_init(&empty[k], TILES);  // the chains that read it
+            mbar_init(&empty[k], 1);
         }
         for (int k = 0; k < PW_PIECES; ++k) mbar_init(&piece[k], 1);
         for (int k = 0; k < 2; ++k) {
@@ -139,12 +144,9 @@ __global__ void __launch_bounds__(PW_NT, 1)
             mbar_init(&p_full[k], 4);
         }
         mbar_init(q_full, 8);
-        mbar_init(o_full, 2);
+        mbar_init(o_full, 1);
         mbar_init(ml_full, 8);
-        mbar_init(&drain[0], 1);
-        mbar_init(&drain[1], 1);
-        mbar_init(&turn[0], 1);
-        mbar_init(&turn[1], 1);
+        mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort = 0;
     }
@@ -249,124 +251,111 @@ __global__ void __launch_bounds__(PW_NT, 1)
             pieces[np % PW_PIECES].steps = 0;
             mbar_arrive(&piece[np % PW_PIECES]);
         }
-        if (!go && lane == 0) {
-            // A wait ran out: let the copies in flight land.  They are the last NS slots issued.
+        if (lane == 0) {
+            // The copies in flight land here even where another warp's wait ran out: they are the last NS
+            // slots issued.
             for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1));
         }
         __syncwarp();
-    } else if (warp == PW_MMA || warp == PW_MMA + 1) {
-        // One thread a chain: nothing here waits for a warp to reconverge, one chain's waits and
-        // commits hide behind the other's products, and a descriptor is its slot's plus a constant
-        // (its address field counts 16 bytes).
-        if (lane == 0) {
-            const int i = warp - PW_MMA;
+    } else if (warp == PW_MMA) {
+        // One lane issues every product, in one order; the warp runs in step (elect_one).  A descriptor is
+        // its slot's plus a constant (its address field counts 16 bytes).
+        const uint32_t it = elect_one();
+        {
             const uint64_t ring = smem_desc(smem_addr(pw_smem + LY::RING), LY::BOX, 1024);
-            const uint64_t qd = smem_desc(smem_addr(pw_smem + LY::Q + (TILES == 2 ? i * LY::SLOT : 0)), LY::BOX, 1024);
+            const uint64_t qd = smem_desc(smem_addr(pw_smem + LY::Q), LY::BOX, 1024);
             constexpr uint32_t IS = mma_desc(128, 128, W::BF, false), IO = mma_desc(128, D, W::BF, true);
-            const uint32_t st = tm + i * 128, ot = tm + 256 + i * 128;
+            using Order = WideOrder<TILES>;
             auto await = [&](uint64_t *bar, uint32_t parity) -> bool {
-                if (paged_wait(smem_addr(bar), parity, abort)) return true;
+                if (__all_sync(0xFFFFFFFFu, paged_wait(smem_addr(bar), parity, abort))) return true;
                 *abort = 1;
                 raise_error(a.err, ERR_TIMEOUT);
                 return false;
             };
-            // The chains take turns, so that one's softmax falls into the other's products (left to
-            // themselves they fall in step, and both wait together: 4500 cycles a step against 3000).
-            uint32_t turns = 0;
-            auto take = [&]() -> bool { return (i == 0 && turns == 0) || await(&turn[i], turns - (i == 0 ? 1u : 0u)); };
-            auto pass = [&]() {
-                mbar_arrive(&turn[i ^ 1]);
-                ++turns;
-            };
-            int j0 = 0;       // slots used before the piece
-            uint32_t ns = 0;  // items so far
+            int j0 = 0;                // slots used before the piece
+            uint32_t ns[2] = {0, 0};   // items of each chain so far
             bool go = true;
             for (int np = 0; go; ++np) {
                 if (!await(&piece[np % PW_PIECES], (uint32_t)(np / PW_PIECES))) break;
                 const PieceDesc pd = pieces[np % PW_PIECES];
                 if (pd.steps == 0) break;
+                const int items = pd.steps * TILES;
                 go = await(q_full, (uint32_t)np);
                 tcgen05_after_sync();
-                // This chain's steps: all, or every other one.
-                constexpr int STRIDE = TILES == 2 ? 1 : 2;
-                const int first = TILES == 2 ? 0 : i;
-                int kx = j0 + WideOrder<TILES>::k(first);  // slot, counted from the start, of the next K
-                auto do_s = [&]() {
-                    const uint64_t kd = ring + (uint32_t)(kx % NS * (LY::SLOT >> 4));
+                // K's slot of an item, filled; S of the item; and what waits for it: the softmax, and the
+                // copies after the step's last item.
+                auto k_slot = [&](int n) { return j0 + Order::k(n / TILES); };
+                auto k_there = [&](int n) -> bool {
+                    const int x = k_slot(n);
+                    return n % TILES != 0 || await(&full[x % NS], (uint32_t)(x / NS));
+                };
+                auto do_s = [&](int n) {
+                    const uint64_t kd = ring + (uint32_t)(k_slot(n) % NS * (LY::SLOT >> 4));
+                    const uint64_t q = qd + (uint32_t)(n % TILES * (LY::SLOT >> 4));
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
                         const int off = ((x / 4) * LY::BOX + (x % 4) * 32) >> 4;
-                        mma_ss(st, qd + off, kd + off, IS, x > 0);
+                        mma_ss(tm + (n & 1) * 128, q + off, kd + off, IS, x > 0, it);
                     }
+                    tcgen05_commit(&s_full[n & 1], it);
+                    if (n % TILES == TILES - 1) tcgen05_commit(&empty[k_slot(n) % NS], it);
                 };
-                auto done_s = [&](int next) {
-                    tcgen05_commit(&s_full[i]);
-                    tcgen05_commit(&empty[kx % NS]);
-                    kx = j0 + WideOrder<TILES>::k(next);
-                };
-                // Turn 0: the first S.  Turn n + 1: P V of the chain's n-th step, S of its next.  Chain 1
-                // takes an empty turn where it has a step less.
-                const bool any = first < pd.steps;
-                if (any && go) go = await(&full[kx % NS], (uint32_t)(kx / NS));
-                if (!go || !(go = take())) break;
-                if (any) do_s();
-                pass();
-                if (any) done_s(first + STRIDE);
-                for (int step = first; step - first < pd.steps && go; step += STRIDE) {
-                    const bool has = step < pd.steps, more = step + STRIDE < pd.steps;
-                    const int vx = j0 + WideOrder<TILES>::v(step, pd.steps), vs = vx % NS;
+#pragma unroll 1
+                for (int n = 0; n < min(2, items) && go; ++n) {
+                    if ((go = k_there(n))) do_s(n);
+                }
+#pragma unroll 1
+                for (int n = 0; n < items && go; ++n) {
+                    const int step = n / TILES, tile = n % TILES, i = n & 1;
                     const int valid = min(PAGED_WIDE_TILE, pd.vis - (pd.tok0 + step * PAGED_WIDE_TILE));
-                    if (has) {
+                    const int vx = j0 + Order::v(step, pd.steps), vs = vx % NS;
+                    if (tile == 0) {
                         if (!(go = await(&full[vs], (uint32_t)(vx / NS)))) break;
                         if (valid & 15) {
                             // V rows of the last 16 tokens that nothing sees may hold anything, NaN too: a
-                            // weight of 0 would keep it.  (Both chains may write these zeros.)
+                            // weight of 0 would keep it.
                             unsigned char *v = pw_smem + LY::RING + vs * LY::SLOT;
 #pragma unroll 1
-                            for (int x = valid * 8; x < ((valid + 15) & ~15) * 8; ++x)
+                            for (int x = valid * 8 + lane; x < ((valid + 15) & ~15) * 8; x += 32)
 #pragma unroll
                                 for (int h = 0; h < LY::HALVES; ++h)
                                     *reinterpret_cast<uint4 *>(v + h * LY::BOX + x * 16) = make_uint4(0u, 0u, 0u, 0u);
                             fence_proxy_async_smem();
+                            __syncwarp();
                         }
-                        if (more && !(go = await(&full[kx % NS], (uint32_t)(kx / NS)))) break;
-                        if (!(go = await(&h_full[i], ns))) break;
                     }
-                    if (!(go = take())) break;
+                    const bool more = n + 2 < items;
+                    if (more && !(go = k_there(n + 2))) break;
+                    const uint32_t pt = tm + i * 128, ot = tm + 256 + i * 128;
+                    const uint64_t vd = ring + (uint32_t)(vs * (LY::SLOT >> 4));
+                    const bool add = step >= (TILES == 2 ? 1 : 2);
+                    if (!(go = await(&h_full[i], ns[i]))) break;
                     tcgen05_after_sync();
-                    if (has) {
-                        const uint64_t vd = ring + (uint32_t)(vs * (LY::SLOT >> 4));
-                        const bool add = step != first;
-                        // The first half of P's tokens, while the softmax writes the second.
-                        if (valid > PAGED_WIDE_TILE - 16) {
+                    // The first half of P's tokens, while the softmax writes the second.
+                    if (valid > PAGED_WIDE_TILE - 16) {
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, add || x > 0);
-                            if (!(go = await(&p_full[i], ns))) break;
-                            tcgen05_after_sync();
+                        for (int x = 0; x < 4; ++x) mma_ts(ot, pt + x * 8, vd + x * 128, IO, add || x > 0, it);
+                        if (!(go = await(&p_full[i], ns[i]))) break;
+                        tcgen05_after_sync();
 #pragma unroll
-                            for (int x = 4; x < 8; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, true);
-                        } else {
-                            if (!(go = await(&p_full[i], ns))) break;
-                            tcgen05_after_sync();
+                        for (int x = 4; x < 8; ++x) mma_ts(ot, pt + x * 8, vd + x * 128, IO, true, it);
+                    } else {
+                        if (!(go = await(&p_full[i], ns[i]))) break;
+                        tcgen05_after_sync();
 #pragma unroll 1
-                            for (int x = 0; x < (valid + 15) / 16; ++x) mma_ts(ot, st + x * 8, vd + x * 128, IO, add || x > 0);
-                        }
-                        ++ns;
-                        if (more) do_s();
+                        for (int x = 0; x < (valid + 15) / 16; ++x) mma_ts(ot, pt + x * 8, vd + x * 128, IO, add || x > 0, it);
                     }
-                    pass();
-                    if (has) {
-                        if (more) done_s(step + 2 * STRIDE);
-                        tcgen05_commit(&empty[vs]);
-                    }
+                    ++ns[i];
+                    if (more) do_s(n + 2);
+                    if (tile == TILES - 1) tcgen05_commit(&empty[vs], it);
                 }
                 if (!go) break;
-                tcgen05_commit(o_full);
+                tcgen05_commit(o_full, it);
                 j0 += 2 * pd.steps;
             }
-            // Nothing of this chain is in flight when the CTA gives its tensor memory back.
-            tcgen05_commit(&drain[i]);
-            if (!mbar_wait_bounded(&drain[i], 0u)) raise_error(a.err, ERR_TIMEOUT);
+            // Nothing is in flight when the CTA gives its tensor memory back.
+            tcgen05_commit(drain, it);
+            if (!mbar_wait_bounded(drain, 0u)) raise_error(a.err, ERR_TIMEOUT);
         }
         __syncwarp();
     } else {
