@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         pdl_trigger();
         // (the queries' place holds nothing yet)
         wk.start(a, l, blockIdx.x, reinterpret_cast<int2 *>(pg_smem + LY::Q), LY::QN * R * LY::QROW / 8);
+        fence_proxy_async_smem();  // these accesses before the queries' copies to the same place
+        __syncwarp();
         // The walk is one piece ahead of the copies, so that a piece's page ids are there when its
         // first step is.
         auto fetch = [&](Piece &p) -> bool {
