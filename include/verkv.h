@@ -396,7 +396,7 @@ typedef struct {
  *   length      device int32 [rows]: how many tokens of each row there are (not read by
  *               verkv_paged_append); 0 is allowed
  *   max_length  an upper bound of every length, known on the host, at most
- *               stride * page_tokens; it sizes the grid, so a graph captured with it serves any
+ *               stride * page_tokens and 2^30; it sizes the grid, so a graph captured with it serves any
  *               lengths up to it */
 typedef struct {
     const int32_t *table;
@@ -424,7 +424,7 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
 /* Attention over the paged cache.  Sequence s has the queries q_start[s] .. q_start[s + 1] - 1, its
  * last tokens: the j-th of c queries sees the first length[s] - c + 1 + j of the sequence's own
  * cached tokens (append first), all tokens of its group's shared prefix, and what `prior` sums up.
- *   seqs, q_tokens  >= 0; q_tokens queries in all
+ *   seqs, q_tokens  >= 0; q_tokens queries in all; at most 65536 sequences, and as many prefixes
  *   q         rows of kv_heads * q_per_kv heads, of the pages' type
  *   q_start   device int32 [seqs + 1], ascending from 0 to q_tokens; NULL: one query a sequence
  *             (q_tokens = seqs)
@@ -433,7 +433,7 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
  *             queries of its group, however many they are.
  *   group_start  device int32 [rows of prefix + 1], ascending from 0 to seqs: sequences
  *             group_start[g] .. group_start[g + 1] - 1 share prefix g; NULL: all share the only one
- *   scale     of the logits, finite; 0: 1 / sqrt(head_dim)
+ *   scale     of the logits, |scale| < 2^127; 0: 1 / sqrt(head_dim)
  *   prior_o, prior_lse  device float [q_tokens][kv_heads * q_per_kv][head_dim] and
  *             [q_tokens][kv_heads * q_per_kv]: attention of the same queries over other tokens, as
  *             verkv_fetch_refine and verkv_attend_dense_host write it, joined to the result; both
@@ -447,7 +447,8 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
  * Logits, the running maximum and sum, and the partial sums are float32; the weights are rounded to
  * the pages' type to be multiplied with V, and not in the sum they are divided by.
  * What pages hold behind a length is never used, but a value that is not finite inside it reaches
- * every query of its sequence, also one whose own place comes before it.
+ * every query of its sequence (or, in a prefix, of its group), also one whose own place comes
+ * before it.
  * A page id outside the pool, a length outside 0 .. max_length, or q_start or group_start not
  * ascending within their range is latched (verkv_sync returns VERKV_EINVAL); nothing outside the
  * tensors is read or written, and the outputs of that call are not valid. */

@@ -116,6 +116,19 @@ def test_long_runs(rows, lengths, prefix):
     Case(lengths, qs=[qs] * len(lengths), prefixes=[prefix] if prefix else (), h=8, g=4, d=64, pt=64).check()
 
 
+@pytest.mark.parametrize("seqs,groups,qs,g", [(2000, 0, 1, 2), (2000, 500, 1, 8), (930, 310, 1, 8), (300, 0, 5, 8), (290, 290, 9, 4)])
+def test_more_segments_than_are_kept_in_shared_memory(seqs, groups, qs, g):
+    at = [i * seqs // max(groups, 1) for i in range(groups)] + [seqs] if groups else None
+    Case([(5 * i) % 39 for i in range(seqs)], qs=[qs] * seqs, prefixes=[(11 * i) % 70 for i in range(groups)], groups=at,
+         h=1, g=g, d=64, pt=16).check()
+
+
+@pytest.mark.parametrize("queries,length,g", [(701, 901, 2), (1100, 1100, 8), (333, 5000, 1)])
+def test_a_prompt_among_decoding_sequences(queries, length, g):
+    # most queries are one sequence's, and the others have one each
+    Case([40, length, 0, 700], qs=[1, queries, 1, 1], prefixes=[129], h=2, g=g, d=128, pt=32).check()
+
+
 @pytest.mark.parametrize("d,dtype,qs", [(64, BF, 1), (128, HF, 1), (128, BF, 3), (64, HF, 5)])
 def test_groups_with_their_own_prefixes(d, dtype, qs):
     # groups of 40, 0, 1, 25 sequences; a prefix without tokens, prefixes without sequences
@@ -353,6 +366,30 @@ def test_refusals():
     assert B.verkv_launch_counts(c.cache.ctx) == n0
     assert go(ws.data_ptr(), need) == B.VERKV_OK  # lse is optional
     c.cache.sync()
+
+
+def test_refusals_of_far_bounds():
+    # a bound whose tokens or steps 31 bits do not count (the table is said to be as wide as that), and a
+    # scale that float32 does not hold in units of log 2
+    c = Case([100, 33, 64], h=2, g=2, d=64, pt=16)
+    n0 = B.verkv_launch_counts(c.cache.ctx)
+    L, q, o = B.lib(), c.cache._rows(c.q, 3, 4, "q"), torch.empty_like(c.q)
+    ws, nbytes = c.cache._space(3, 0, 3)
+    for bound, scale in ((1 << 30, 3e38), ((1 << 30) + 1, 0.0), ((1 << 31) - 1, 0.0), (100, -3e38)):
+        own = B.verkv_span(c.table.data_ptr(), 3, 1 << 27, c.lengths.data_ptr(), bound)
+        assert L.verkv_paged_attend(c.cache.ctx, c.cache._layer(0), 3, 3, q, None, own, None, None, scale, None, None,
+                                    o.data_ptr(), None, ws, nbytes) == B.VERKV_EINVAL
+    assert B.verkv_launch_counts(c.cache.ctx) == n0
+    c.cache.sync()
+
+
+def test_devices_without_an_index():
+    c = Case([20, 3], h=1, g=2, d=64)
+    rope = Rope([1.0] * 32, device="cuda")
+    assert rope.dev == c.cache.dev == PagedKV(1, 2, 64, device="cuda").dev
+    q, _ = c.cache.norm_rotate(c.q, None, ints([0, 0]), rope)
+    c.cache.sync()
+    assert torch.equal(q, c.q)
 
 
 def test_the_callers_device_is_left_as_it_was():

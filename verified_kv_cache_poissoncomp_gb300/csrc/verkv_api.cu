@@ -477,7 +477,8 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
         l.cost += likely * (l.grouped ? long_each * (l.tall ? 2.0 : 1.5) : 1.0 * long_each + 1.6);
     }
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
-    if (steps >= (1LL << 31) || units + l.ctas >= (1LL << 31)) return false;
+    // (a run's end is its start plus a run's length, which the last run may pass by a step a CTA)
+    if (steps >= (1LL << 31) - 2 * PAGED_MAX_CTAS || units + l.ctas >= (1LL << 31)) return false;
     l.slots = (int)(units + l.ctas);
     auto take = [&](size_t bytes) {
         unsigned char *p = ws + off;
@@ -1171,13 +1172,14 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
     if (seqs == 0 && q_tokens != 0) return fail(ctx, VERKV_EINVAL, "paged_attend: queries of no sequence");
     auto bad_span = [&](const verkv_span *s) {
         return !s->table || !s->length || bad4(s->table) || bad4(s->length) || s->rows < 1 || s->stride < 1 || s->max_length < 0 ||
-               (int64_t)s->max_length > (int64_t)s->stride * pages->page_tokens;
+               s->max_length > (1 << 30) || (int64_t)s->max_length > (int64_t)s->stride * pages->page_tokens;
     };
     if (seqs > 0 && own && (bad_span(own) || own->rows != seqs)) return fail(ctx, VERKV_EINVAL, "paged_attend: bad table of the sequences' own tokens");
     if (prefix && bad_span(prefix)) return fail(ctx, VERKV_EINVAL, "paged_attend: bad table of the shared prefixes");
     if (prefix && !group_start && groups != 1) return fail(ctx, VERKV_EINVAL, "paged_attend: several prefixes need group_start");
     if (group_start && !prefix) return fail(ctx, VERKV_EINVAL, "paged_attend: group_start without prefixes");
-    if (!isfinite(scale)) return fail(ctx, VERKV_EINVAL, "paged_attend: scale must be finite");
+    const float scale_log2 = (float)((scale == 0.0f ? 1.0 / sqrt((double)sh.head_dim) : (double)scale) * 1.4426950408889634);
+    if (!isfinite(scale_log2)) return fail(ctx, VERKV_EINVAL, "paged_attend: scale must be finite, also in units of log 2");
     if ((prior_o == nullptr) != (prior_lse == nullptr)) return fail(ctx, VERKV_EINVAL, "paged_attend: prior_o and prior_lse come together");
     if (bad_rows(q)) return fail(ctx, VERKV_EINVAL, "paged_attend: rows need 16-byte alignment and strides >= 0 that are multiples of 8");
     if (bad16(prior_o) || bad16(o_out) || bad4(prior_lse) || bad4(lse_out) || bad4(q_start) || bad4(group_start))
@@ -1207,7 +1209,7 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
     a.g_shift = log2_of(sh.q_per_kv);
     a.page_shift = log2_of(pages->page_tokens);
     a.num_pages = pages->num_pages;
-    a.scale_log2 = (float)((scale == 0.0f ? 1.0 / sqrt((double)sh.head_dim) : (double)scale) * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.err = ctx->err;
     a.prior_o = prior_o;
     a.prior_lse = prior_lse;

@@ -26,7 +26,9 @@ class Rope:
 
     def __init__(self, inv_freq, interleaved=False, device=None):
         f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").reshape(-1).tolist()
-        self.dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.dev = torch.device("cuda" if device is None else device)
+        if self.dev.index is None:
+            self.dev = torch.device("cuda", torch.cuda.current_device())
         turns = torch.frombuffer(B.verkv_rope_turns(f), dtype=torch.int64) if f else torch.empty(0, dtype=torch.int64)
         self.turns = turns.to(self.dev)
         self.desc = B.verkv_rope(2 * len(f), int(bool(interleaved)), self.turns.data_ptr())
@@ -51,7 +53,7 @@ class PagedKV:
             layers, num_pages, page_tokens = kv.shape[0], kv.shape[1], kv.shape[3]
         if dtype not in _DTYPES:
             raise ValueError("dtype: torch.bfloat16 or torch.float16")
-        self.dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.dev = torch.device("cuda" if device is None else device)
         if self.dev.index is None:
             self.dev = torch.device("cuda", torch.cuda.current_device())
         self.dtype, self.h, self.hq, self.d = dtype, kv_heads, kv_heads * q_per_kv, head_dim
