@@ -123,6 +123,20 @@ def test_more_segments_than_are_kept_in_shared_memory(seqs, groups, qs, g):
          h=1, g=g, d=64, pt=16).check()
 
 
+@pytest.mark.parametrize("prefixes", [[5000, 4990, 4999], [3000, 0, 2900], [700, 600, 650, 1], [1, 0, 0, 9000], [128, 129], [0, 0]])
+@pytest.mark.parametrize("qs,g", [(1, 4), (9, 8), (40, 4)])
+def test_few_groups_of_unequal_prefixes(prefixes, qs, g):
+    # few units, which may each get as many runs of the line: some runs have nothing to do
+    n = len(prefixes)
+    Case([(37 * i) % 150 for i in range(6 * n)], qs=[qs] * (6 * n), prefixes=prefixes, groups=[6 * i for i in range(n + 1)],
+         h=2, g=g, d=64, pt=64).check()
+
+
+@pytest.mark.parametrize("lengths,qs", [([5000], [70]), ([5000, 4700], [33, 34]), ([900, 0, 910], [40, 1, 50]), ([4000, 3990], [300, 1])])
+def test_few_long_sequences_with_many_queries(lengths, qs):
+    Case(lengths, qs=qs, h=2, g=4, d=128, pt=32).check()
+
+
 @pytest.mark.parametrize("queries,length,g", [(701, 901, 2), (1100, 1100, 8), (333, 5000, 1)])
 def test_a_prompt_among_decoding_sequences(queries, length, g):
     # most queries are one sequence's, and the others have one each

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
     if (warp == PG_CONS) {
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
         const int box = min(1 << a.page_shift, PAGED_TILE);  // tokens of a page in one step
-        PagedWalk wk;
+        PagedWalk<false> wk;
         // (the other kernel of the call lets this one start when it has waited itself)
         if (wait_first) pdl_wait();
         pdl_trigger();
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
         const int r = own ? s : a.group_start ? last_at_most(a.group_start, a.level[0].rows, s) : 0;
         if (r < 0 || r >= a.level[own].rows) continue;
         const int i = r + (own && l.with[0] ? a.level[0].rows : 0);
-        const int per = l.rec[0].x;
+        const int per = l.rec[0].x, room = l.rec[0].y;
         const int2 before = l.rec[1 + i];
         bool bad = false;
         const PagedSeg sg = paged_segment(a, l, i, bad);
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
         if (j < 0 || j >= sg.qn || per <= 0) continue;  // (per 0: a bad segment, nothing was done)
         const int mt = j >> l.tt_shift, steps = paged_steps(sg, l, mt);
         if (steps == 0) continue;
-        const int w0 = before.x + paged_steps_before(sg, l, mt) * a.hkv + head * steps;
+        const int w0 = before.x + paged_steps_before(sg, l, mt, room) * a.hkv + head * (room ? room : steps);
         const int c0 = (unsigned)w0 / (unsigned)per, c1 = (unsigned)(w0 + steps - 1) / (unsigned)per;
         const int in = ((j - (mt << l.tt_shift)) << a.g_shift) + g;
         const int slot = clampi(c0 + before.y + mt * a.hkv + head, 0, l.slots - 1);
@@ -583,7 +583,7 @@ cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorM
 
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLines &lines, int dtype, int d, cudaStream_t s) {
     const long long rows = (long long)a.q_tokens * (a.hkv << a.g_shift);
-    // Few rows with many partials each (39 of 128 rows, 128K tokens: 98 -> 91 us a call) have warps to spare.
+    // Few rows with many partials each (128 rows with 39 each, 128K tokens: 100 -> 93 us a call) have warps to spare.
     double partials = 0.0;  // of a row, about
     for (const PagedLine &l : lines.l)
         if (l.units > 0) partials = std::max(partials, (double)l.ctas / l.units);

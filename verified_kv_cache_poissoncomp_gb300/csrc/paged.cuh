@@ -6,8 +6,12 @@
 // head and one tile of up to `tt` query tokens, all q_per_kv heads of each.  A unit's work is the
 // number of `tile`-token steps over what its last query sees.  All units' work, laid end to end
 // (segment, row tile, head, step), is cut into equal runs of `per` steps, one for each CTA, wherever
-// the cuts fall: however uneven the lengths are, no CTA has more than `per` steps, a long unit is shared by many CTAs and a CTA takes many short ones.  Lengths are read on
-// the device, so a captured graph follows them.  The piece of unit u in run c goes to the partial
+// the cuts fall: however uneven the lengths are, no CTA has more than `per` steps, a long unit is
+// shared by many CTAs and a CTA takes many short ones.  A run that holds the end of one unit and the
+// start of the next costs a CTA about PAGED_SLACK steps more than one piece of the same length: where
+// units are few, each gets the same whole number of runs (`room` steps of the line, its own or not),
+// if they need not be longer by more than that (8 sequences behind 40000 tokens 49.3 -> 43.5 us, 32
+// behind 20000 35.7 -> 31.4).  Lengths are read on the device, so a captured graph follows them.  The piece of unit u in run c goes to the partial
 // slot c + u: walking the line, each step to the next piece raises exactly one of the two.  Row tiles
 // come before heads so that the CTAs which read the same K and V for other rows do so at about the
 // same time, from the L2 cache (heads first, 1024 rows read a 134 MB prefix four times from memory).
@@ -58,7 +62,7 @@ struct PagedLine {
     int slots;                  // partial slots there is room for
     int tall;                   // (host: tiles of 256 rows)
     double cost, units;         // (host: us of one SM; about how many units)
-    int2 *rec;                  // {per, 0}, then {work before, units before} of each segment with work; per 0: a bad segment, no work
+    int2 *rec;                  // {per, room}, then {work before, units before} of each segment with work; per 0: a bad segment, no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
     float *part_o;
     float *part_ml;             // [slots][tt * G][2]: running maximum (log2 units) and sum
@@ -83,6 +87,7 @@ constexpr int PAGED_TILE = 64;        // tokens of a step of k_paged
 constexpr int PAGED_ROWS = 32;        // most rows of its units (16 or 32)
 constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
 constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
+constexpr int PAGED_SLACK = 2;        // steps a run may be longer for units of whole runs
 
 cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long long rows, int d, int box_rows);
 // wait_first false: the launch before it on the stream is this call's other kernel, which it need not
@@ -150,9 +155,9 @@ __device__ __forceinline__ int paged_visible(const PagedSeg &s, const PagedLine 
 __device__ __forceinline__ int paged_steps(const PagedSeg &s, const PagedLine &l, int m) {
     return (paged_visible(s, l, m) + (1 << l.tile_shift) - 1) >> l.tile_shift;
 }
-// Steps of all row tiles before m, for one head.
-__device__ __forceinline__ int paged_steps_before(const PagedSeg &s, const PagedLine &l, int m) {
-    if (!s.own) return m * paged_steps(s, l, 0);
+// What all row tiles before m take of the line, for one head.  (A room is given to every unit or none.)
+__device__ __forceinline__ int paged_steps_before(const PagedSeg &s, const PagedLine &l, int m, int room) {
+    if (!s.own || room) return m * (room ? room : paged_steps(s, l, 0));
     int w = 0;
 #pragma unroll 1
     for (int i = 0; i < m; ++i) w += paged_steps(s, l, i);
@@ -162,8 +167,12 @@ __device__ __forceinline__ int paged_steps_before(const PagedSeg &s, const Paged
 // One warp's walk over the run of this CTA.  A kernel calls start() and next() at one place each: a
 // launch begins with cold instruction caches and fetches its code line by line, so its size is time.  All lanes hold the same values.  The host has checked
 // that a whole line's steps and units fit 31 bits; a segment outside its range empties the line.
+// ROOMS: units may be given rooms.  (k_paged's runs change units at less cost, and its start at more:
+// with rooms 8 sequences of up to 512 tokens took 11.1 us for 10.7.)
+template <bool ROOMS>
 struct PagedWalk {
     int w, w1;   // next step, end of the run
+    int room;    // of every unit on the line, or 0: its steps
     int Wx, Ux;  // work and units before the segment
     int per_head;
     int seg, n, nt;
@@ -175,7 +184,7 @@ struct PagedWalk {
         bool bad = false;
         s = paged_segment(a, l, seg, bad);
         nt = paged_row_tiles(s, l);
-        per_head = paged_steps_before(s, l, nt);
+        per_head = paged_steps_before(s, l, nt, ROOMS ? room : 0);
     }
 
     // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also writes
@@ -185,21 +194,39 @@ struct PagedWalk {
         const int lane = threadIdx.x & 31;
         n = paged_segments(a, l);
         seg = n;
-        w = w1 = 0;
+        w = w1 = room = 0;
         bool bad = false;
         int total = 0;
 #pragma unroll 4
         for (int i = lane; i < n; i += 32) {
             const PagedSeg g = paged_segment(a, l, i, bad);
-            const int t = paged_row_tiles(g, l), h = paged_steps_before(g, l, t);
+            const int t = paged_row_tiles(g, l), h = paged_steps_before(g, l, t, 0);
             total += h;
             if (i < cap) cache[i] = make_int2(h, t);
         }
         total = __reduce_add_sync(0xFFFFFFFFu, total) * a.hkv;
         bad = __any_sync(0xFFFFFFFFu, bad);
-        const int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
+        int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
+        if (ROOMS && n <= 32 && per > 0 && per < 1 << 20) {
+            // A lane a segment.  (Quotients by the fast reciprocal, put right where they must be exact.)
+            const int2 g = lane < n ? cache[lane] : make_int2(0, 0);
+            const int units = __reduce_add_sync(0xFFFFFFFFu, g.y) * a.hkv;
+            if (units <= l.ctas && total > 0) {
+                const int runs = (int)__fdividef(l.ctas + 0.5f, (float)units);
+                // row tiles of a sequence's own tokens differ: their sum is more than any
+                const int each = lane >= (l.with[0] ? a.level[0].rows : 0) ? g.x : (int)(__fdividef((float)g.x, (float)max(g.y, 1)) + 1.0f);
+                const int longest = __reduce_max_sync(0xFFFFFFFFu, each);
+                const int p = (int)__fdividef((float)(longest + runs), (float)runs);
+                if (p <= per + PAGED_SLACK) {
+                    per = p;
+                    room = runs * p;
+                    total = units * room;
+                    if (lane < n) cache[lane].x = g.y * room;
+                }
+            }
+        }
         if (c == 0 && lane == 0) {
-            l.rec[0] = make_int2(per, 0);
+            l.rec[0] = make_int2(per, room);
             if (bad) raise_error(a.err, ERR_PAGE);
         }
         if (bad) return;
@@ -217,7 +244,7 @@ struct PagedWalk {
             } else if (i < n) {
                 const PagedSeg g = paged_segment(a, l, i, bad);
                 gt = paged_row_tiles(g, l);
-                gh = paged_steps_before(g, l, gt);
+                gh = paged_steps_before(g, l, gt, 0);  // (no rooms with as many)
             }
             const int mw = gh * a.hkv, mu = gt * a.hkv;
             int sw = mw, su = mu;  // inclusive sums over the lanes
@@ -257,25 +284,26 @@ struct PagedWalk {
         if (w == Wx && (threadIdx.x & 31) == 0) l.rec[1 + seg] = make_int2(Wx, Ux);
         int r = w - Wx;
         m = 0;
-        int steps = paged_steps(s, l, 0);
-        if (!s.own) {
-            m = (unsigned)r / (unsigned)(steps * a.hkv);
-            r -= m * steps * a.hkv;
+        int steps = paged_steps(s, l, 0), span = ROOMS && room ? room : steps;
+        if (!s.own || (ROOMS && room)) {
+            m = (unsigned)r / (unsigned)(span * a.hkv);
+            r -= m * span * a.hkv;
+            if (ROOMS && s.own) steps = paged_steps(s, l, m);
         } else {
 #pragma unroll 1
-            while (r >= steps * a.hkv) {
-                r -= steps * a.hkv;
+            while (r >= span * a.hkv) {
+                r -= span * a.hkv;
                 if (++m >= nt) return false;  // lengths changed under the kernel
-                steps = paged_steps(s, l, m);
+                span = steps = paged_steps(s, l, m);
             }
         }
-        head = (unsigned)r / (unsigned)steps;
-        r -= head * steps;
+        head = (unsigned)r / (unsigned)span;
+        r -= head * span;
         t0 = r;
         t1 = min(steps, r + (w1 - w));
         slot = c + Ux + m * a.hkv + head;
-        w += t1 - t0;
-        return true;
+        w += min(span - r, w1 - w);
+        return t0 < t1;  // (a run behind the end of a unit with room has nothing to do)
     }
 };
 

@@ -432,8 +432,8 @@ int64_t paged_rows(int64_t q_tokens, int64_t segments, int G) { return (q_tokens
 
 // Which kernel a level goes through, by the rows of its segments.  Prefixes of up to 16 rows and own
 // tokens of up to 32: k_paged; more: k_paged_wide.  (32 rows of a 32K prefix: k_paged 52 us, reading at
-// 4.5 TB/s for its arithmetic, k_paged_wide 44; own tokens of 32 sequences of 18 rows, up to 4096 each:
-// k_paged 61, k_paged_wide, whose 128 rows are then mostly empty, 94.)
+// 4.5 TB/s for its arithmetic, k_paged_wide 40; own tokens of 32 sequences of 18 rows, up to 4096 each:
+// k_paged 58, k_paged_wide, whose 128 rows are then mostly empty, 77.)
 bool paged_wide_prefix(int64_t rows) { return rows > PAGED_ROWS / 2; }
 bool paged_wide_own(int64_t rows) { return rows > PAGED_ROWS; }
 
@@ -493,9 +493,9 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
 
 // The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, so that one
 // after the other each leaves the GPU idle while it starts and ends, some 10 us.  Where k_paged's work
-// is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 64 -> 45 us, 64
-// sequences 86 -> 74); but alone on an SM it takes longer in all, so where its work would fill the
-// GPU for 30 us it follows on all of it (256 sequences: 178 against 201 us side by side).  Costs are
+// is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 46 -> 39 us, 64
+// sequences 77 -> 74); but alone on an SM it takes longer in all, so where its work would fill the
+// GPU for 30 us it comes first, on all of it (256 sequences: 158 against 170 us side by side).  Costs are
 // the us of a step: 1.0 of k_paged alone on an SM beside k_paged_wide, and 1.6 a unit; 1.5 or 2 of
 // k_paged_wide with 128 or 256 rows.
 bool paged_share(PagedLine &wide, PagedLine &own, int sms) {
