@@ -18,6 +18,10 @@
 // values; it loads them all, makes the token's sines once, folds the norm's weights into them --
 //   out_a = s (x_a (w_a cos) - x_b (w_b sin)),  out_b = s (x_b (w_b cos) + x_a (w_a sin)),  s = 1 / rms
 // -- and then spends three packed operations a channel pair.
+//
+// Measured: 32768 tokens of 40 heads of 128 (671 MB) 104 us, 0.95 of a plain copy's bandwidth; 32768
+// tokens' keys and values into pages (268 MB) 47 us, 0.85; 8 tokens 2.1 us and 1021 small ones 3.1, a
+// launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -9,10 +9,15 @@
 // unit's queries beside its first step; what a step is (which rows, which tokens, whether a unit
 // begins or ends with it) travels with it, so one warp's walk drives the CTA and runs ahead of it.
 // Four warps take 16 tokens of a step each (with 32 rows: two take each half of the rows, 32 tokens
-// each): S = Q K^T with the rows as the m16 of mma.m16n8k16 (K by ldmatrix), the softmax in registers -- each warp keeps its own running maximum and sum and rescales
-// only when some row's maximum rises -- and P, already in the A operand's layout, times V (ldmatrix,
-// transposed).  At a unit's end the four warps' states are joined in the step's own shared memory,
+// each): S = Q K^T with the rows as the m16 of mma.m16n8k16 (K by ldmatrix), the softmax in registers
+// -- each warp keeps its own running maximum and sum and rescales only when some row's maximum rises --
+// and P, already in the A operand's layout, times V (ldmatrix, transposed).  At a unit's end the four warps' states are joined in the step's own shared memory,
 // which nothing reads any more, and written as one partial.
+//
+// Measured (d 128, 8 heads, bf16): 32 sequences of up to 16384 tokens (1.1 GB) 168 us a call, 0.97 of a
+// plain copy's bandwidth; 4 behind 128K tokens 93 us, 0.87; 256 sequences of up to 256 tokens 44 us
+// (41 without any arithmetic: their copies, of whole steps, and the start bound it); 8 of up to 512
+// tokens 10.5 us, two launches.
 //
 // k_paged_merge: a warp, or with few rows four, per query token and head joins the partials of its
 // prefix and its own pages, and the caller's prior state, in a fixed order.

@@ -24,6 +24,14 @@
 // maximum less SHIFT, and is raised -- with O scaled in tensor memory -- only when the maximum has
 // risen by more than SLACK since: rarely after the first steps, and no weight passes
 // 2^(SHIFT + SLACK) <= 2^14.  fp16 weights sit 2^8 up, away from its subnormals.
+//
+// Measured (8 heads, d 128, bf16; whole calls): 1024 rows a head behind 128K tokens 405 us,
+// 1.36 PFLOP/s, 0.71 of a library matrix product's rate; behind 32K tokens 120 us; 32 rows behind 128K
+// 91 us, 0.87 of a plain copy's bandwidth.  A step of 256 rows takes about 3300 cycles.  Its products
+// need 2050 at the tensor core's rate and some 2500 with their operands' reads from shared memory
+// (Q K^T: 82 cycles for 64), and it is they that bound it: a faster maximum, or P announced in smaller
+// parts, changed nothing or lost (the smaller parts 4 %), and Q K^T in two halves lost 25 %.  With
+// d 64 the products halve and the exponentials do not (32K tokens, 1024 rows: 98 us).
 #include <float.h>
 #include <math.h>
 

@@ -165,8 +165,9 @@ __device__ __forceinline__ int paged_steps_before(const PagedSeg &s, const Paged
 }
 
 // One warp's walk over the run of this CTA.  A kernel calls start() and next() at one place each: a
-// launch begins with cold instruction caches and fetches its code line by line, so its size is time.  All lanes hold the same values.  The host has checked
-// that a whole line's steps and units fit 31 bits; a segment outside its range empties the line.
+// launch begins with cold instruction caches and fetches its code line by line, so its size is time.
+// All lanes hold the same values.  The host has checked that a whole line's steps and units fit 31
+// bits; a segment outside its range empties the line.
 // ROOMS: units may be given rooms.  (k_paged's runs change units at less cost, and its start at more:
 // with rooms 8 sequences of up to 512 tokens took 11.1 us for 10.7.)
 template <bool ROOMS>
@@ -188,8 +189,8 @@ struct PagedWalk {
     }
 
     // Places the walk at the start of run `c`.  Called by a whole warp; the warp of run 0 also writes
-    // how long a run is and reports bad segments.  First the whole
-    // line's steps, keeping each segment's in shared memory (`cap` of them) as it goes, then the place.
+    // how long a run is and reports bad segments.  First the whole line's steps, keeping each segment's
+    // in shared memory (`cap` of them, at least 32) as it goes, then the place.
     __device__ __forceinline__ void start(const PagedArgs &a, const PagedLine &l, int c, int2 *cache, int cap) {
         const int lane = threadIdx.x & 31;
         n = paged_segments(a, l);
