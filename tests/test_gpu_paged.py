@@ -221,6 +221,19 @@ def test_not_a_number_stays_in_its_sequence():
     assert bool(torch.isnan(o3[2, 0]).all()) and bool(torch.isnan(lse3[2, 0])) and torch.equal(o3[2, 1:], o[2, 1:])
 
 
+@pytest.mark.parametrize("d,dtype,lengths", [(128, HF, (300, 60)), (64, BF, (300, 60)), (128, BF, (1200, 9, 40)), (64, HF, (129, 1, 128))])
+def test_same_bits_with_units_of_one_step_behind_longer_ones(d, dtype, lengths):
+    # a run of the line holds many units, and the warps that share a unit leave it at their own times
+    n = 132
+    c = Case(list(lengths) * (n // len(lengths)), qs=[9] * n, h=8, g=8, d=d, dtype=dtype, pt=64)
+    o, lse = c.check()
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(1500):
+        o1, lse1 = c.run()
+        bad += (o1 != o).any() | (lse1 != lse).any()
+    assert not bad.item()
+
+
 def test_same_bits_again_and_whatever_the_bound():
     c = Case([300, 5, 800, 64] * 10, prefixes=[2000], h=2, g=4)
     o, lse = c.run()

@@ -474,7 +474,9 @@ __global__ void __launch_bounds__(PW_NT, 1)
             }
             if (!ok) break;
             if (TILES == 1) {
-                // Each chain tells the other its rows' reference and sum.
+                // Each chain tells the other its rows' reference and sum, once all eight warps have read those
+                // of the unit before: a first product of this unit says so, and a chain without one asks.
+                if (count == 0 && !wait(q_full, (uint32_t)np)) break;
                 ml[(i * 128 + r) * 2] = ref;
                 ml[(i * 128 + r) * 2 + 1] = sum;
                 __syncwarp();
