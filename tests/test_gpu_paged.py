@@ -132,6 +132,12 @@ def test_few_groups_of_unequal_prefixes(prefixes, qs, g):
          h=2, g=g, d=64, pt=64).check()
 
 
+@pytest.mark.parametrize("qs", [[1] * 5, [9, 30, 9, 0, 12]])
+@pytest.mark.parametrize("groups", [[0, 0, 5, 5], [0, 2, 2, 5], [0, 0, 0, 5], [0, 5, 5, 5]])
+def test_groups_without_sequences(groups, qs):
+    Case([70, 0, 5, 300, 129], qs=qs, prefixes=[900, 333, 64], groups=groups, h=2, g=4, d=64, pt=32).check()
+
+
 @pytest.mark.parametrize("lengths,qs", [([5000], [70]), ([5000, 4700], [33, 34]), ([900, 0, 910], [40, 1, 50]), ([4000, 3990], [300, 1])])
 def test_few_long_sequences_with_many_queries(lengths, qs):
     Case(lengths, qs=qs, h=2, g=4, d=128, pt=32).check()
