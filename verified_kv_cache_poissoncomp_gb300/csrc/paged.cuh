@@ -10,9 +10,10 @@
 // shared by many CTAs and a CTA takes many short ones.  A run that holds the end of one unit and the
 // start of the next costs a CTA about PAGED_SLACK steps more than one piece of the same length: where
 // units are few, each gets the same whole number of runs (`room` steps of the line, its own or not),
-// if they need not be longer by more than that (8 sequences behind 40000 tokens 49.3 -> 43.5 us, 32
-// behind 20000 35.7 -> 31.4).  Lengths are read on the device, so a captured graph follows them.  The piece of unit u in run c goes to the partial
-// slot c + u: walking the line, each step to the next piece raises exactly one of the two.  Row tiles
+// if they need not be longer by more than that (8 sequences behind 40000 tokens 48.5 -> 43.6 us, 64
+// behind 32768 73.8 -> 68.3).  Lengths are read on the device, so a captured graph follows them.
+//
+// The piece of unit u in run c goes to the partial slot c + u: walking the line, each step to the next piece raises exactly one of the two.  Row tiles
 // come before heads so that the CTAs which read the same K and V for other rows do so at about the
 // same time, from the L2 cache (heads first, 1024 rows read a 134 MB prefix four times from memory).
 #pragma once
@@ -209,15 +210,17 @@ struct PagedWalk {
         bad = __any_sync(0xFFFFFFFFu, bad);
         int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
         if (ROOMS && n <= 32 && per > 0 && per < 1 << 20) {
-            // A lane a segment.  (Quotients by the fast reciprocal, put right where they must be exact.)
+            // A lane a segment.  (Quotients by the fast reciprocal, whose error of two units of the last place
+            // is less than the halves added here; p is put right if not.)
             const int2 g = lane < n ? cache[lane] : make_int2(0, 0);
             const int units = __reduce_add_sync(0xFFFFFFFFu, g.y) * a.hkv;
             if (units <= l.ctas && total > 0) {
                 const int runs = (int)__fdividef(l.ctas + 0.5f, (float)units);
                 // row tiles of a sequence's own tokens differ: their sum is more than any
-                const int each = lane >= (l.with[0] ? a.level[0].rows : 0) ? g.x : (int)(__fdividef((float)g.x, (float)max(g.y, 1)) + 1.0f);
+                const int each = lane >= (l.with[0] ? a.level[0].rows : 0) ? g.x : (int)(__fdividef((float)g.x, (float)max(g.y, 1)) + 0.5f);
                 const int longest = __reduce_max_sync(0xFFFFFFFFu, each);
-                const int p = (int)__fdividef((float)(longest + runs), (float)runs);
+                int p = (int)__fdividef(longest + runs - 0.5f, (float)runs);
+                p += p * runs < longest ? 1 : 0;
                 if (p <= per + PAGED_SLACK) {
                     per = p;
                     room = runs * p;

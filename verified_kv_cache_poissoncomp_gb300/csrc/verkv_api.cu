@@ -493,11 +493,11 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
 
 // The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, so that one
 // after the other each leaves the GPU idle while it starts and ends, some 10 us.  Where k_paged's work
-// is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 46 -> 39 us, 64
-// sequences 77 -> 74); but alone on an SM it takes longer in all, so where its work would fill the
-// GPU for 30 us it comes first, on all of it (256 sequences: 158 against 170 us side by side).  Costs are
-// the us of a step: 1.0 of k_paged alone on an SM beside k_paged_wide, and 1.6 a unit; 1.5 or 2 of
-// k_paged_wide with 128 or 256 rows.
+// is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 46 -> 40 us); but
+// alone on an SM it takes longer in all, so where its work would fill the GPU for 30 us it comes first,
+// on all of it (256 sequences: 158 against 170 us side by side).  Costs are the us of a step: 1.0 of
+// k_paged alone on an SM beside k_paged_wide, and 1.6 a unit; 1.5 or 2 of k_paged_wide with 128 or 256
+// rows.
 bool paged_share(PagedLine &wide, PagedLine &own, int sms) {
     const double w = wide.cost, o = own.cost;
     const int x = (int)(sms * o / (w + o)) + 1;
