@@ -471,10 +471,11 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
         steps += tiles * hkv * each;
         segs += lv.rows;
         // What paged_share goes by: prefixes are taken to be of the bound's length, own tokens of half.
-        const double likely = (double)hkv * std::max<int64_t>(a.q_tokens >> l.tt_shift, lv.rows);
+        const int64_t each_row = (a.q_tokens + lv.rows - 1) / lv.rows;
+        const double likely = (double)hkv * lv.rows * ((each_row + (1 << l.tt_shift) - 1) >> l.tt_shift);
         const double long_each = x == 0 ? (double)each : 0.5 * (each + 1);
         l.units += likely;
-        l.cost += likely * (l.grouped ? long_each * (l.tall ? 2.0 : 1.5) : 1.0 * long_each + 1.6);
+        l.cost += likely * (l.grouped ? long_each * (l.tall ? 2.0 : 1.5) : (rows_tile > 16 ? 1.8 : 1.0) * (0.4 * long_each + 0.7));
     }
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
     // (a run's end is its start plus a run's length, which the last run may pass by a step a CTA)
@@ -491,18 +492,23 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     return true;
 }
 
-// The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, so that one
-// after the other each leaves the GPU idle while it starts and ends, some 10 us.  Where k_paged's work
-// is small it gets SMs of its own beside the others (8 sequences behind 32K tokens: 46 -> 40 us); but
-// alone on an SM it takes longer in all, so where its work would fill the GPU for 30 us it comes first,
-// on all of it (256 sequences: 158 against 170 us side by side).  Costs are the us of a step: 1.0 of
-// k_paged alone on an SM beside k_paged_wide, and 1.6 a unit; 1.5 or 2 of k_paged_wide with 128 or 256
-// rows.
+// The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, and one
+// after the other each leaves the GPU idle while it starts and ends, and the one bound by bytes the
+// tensor cores of the other.  So k_paged gets SMs of its own beside the others, in proportion to the
+// work (8 sequences behind 32K tokens: 46 us one after the other, 40 side by side; 256: 158, 144; 128
+// with up to 1000 tokens of their own: 119, 98), unless it would take most of them.  Costs are the us
+// of a step on an SM: 0.4 of k_paged, two CTAs an SM, and 0.7 a unit, with 32 rows 1.8 times that; 1.5
+// or 2 of k_paged_wide with 128 or 256 rows.
 bool paged_share(PagedLine &wide, PagedLine &own, int sms) {
     const double w = wide.cost, o = own.cost;
-    const int x = (int)(sms * o / (w + o)) + 1;
-    if (x > sms * 3 / 4 || o > 30.0 * sms) return false;
-    own.ctas = std::min(own.ctas, x);
+    int x = (int)(sms * o / (w + o)) + 1;
+    if (x > sms * 3 / 4) return false;
+    // Whole runs for each unit of k_paged_wide, where that takes little from either.
+    const int n = sms - x, units = (int)std::min<double>(wide.units, sms);
+    const int less = n / units * units, more = less + units;
+    if (more - n <= x / 5) x = sms - more;
+    else if (n - less <= n / 8) x = sms - less;
+    own.ctas = std::min(own.ctas, 2 * x);
     wide.ctas = std::min(wide.ctas, sms - x);
     return true;
 }
