@@ -495,7 +495,7 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
 // The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, and one
 // after the other each leaves the GPU idle while it starts and ends, and the one bound by bytes the
 // tensor cores of the other.  So k_paged gets SMs of its own beside the others, in proportion to the
-// work (8 sequences behind 32K tokens: 46 us one after the other, 40 side by side; 256: 158, 144; 128
+// work (8 sequences behind 32K tokens: 43 us one after the other, 40 side by side; 256: 158, 143; 128
 // with up to 1000 tokens of their own: 119, 98), unless it would take most of them.  Costs are the us
 // of a step on an SM: 0.4 of k_paged, two CTAs an SM, and 0.7 a unit, with 32 rows 1.8 times that; 1.5
 // or 2 of k_paged_wide with 128 or 256 rows.
