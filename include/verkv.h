@@ -444,8 +444,10 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
  *             where a query sees nothing
  *   workspace device, 256-byte aligned, at least verkv_paged_workspace_size bytes; calls that may
  *             run at the same time (graphs replayed on other streams among them) need one each
- * Logits, the running maximum and sum, and the partial sums are float32; the weights are rounded to
- * the pages' type to be multiplied with V, and not in the sum they are divided by.
+ * Logits, the running maximum and sum, and the partial sums are float32.  The weights are multiplied
+ * with V as two parts of the pages' type, which hold them to 2^-16 (bf16) or 2^-22 (fp16); where
+ * prefixes or sequences have more than 128 rows (queries x q_per_kv) on average, they are rounded to
+ * the pages' type instead, and not in the sum they are divided by.
  * What pages hold behind a length is never used, but a value that is not finite inside it reaches
  * every query of its sequence (or, in a prefix, of its group), also one whose own place comes
  * before it.

@@ -11,8 +11,13 @@
 // Four warps take 16 tokens of a step each (with 32 rows: two take each half of the rows, 32 tokens
 // each): S = Q K^T with the rows as the m16 of mma.m16n8k16 (K by ldmatrix), the softmax in registers
 // -- each warp keeps its own running maximum and sum and rescales only when some row's maximum rises --
-// and P, already in the A operand's layout, times V (ldmatrix, transposed).  At a unit's end the four warps' states are joined in the step's own shared memory,
-// which nothing reads any more, and written as one partial.
+// and P, already in the A operand's layout, times V (ldmatrix, transposed).  A weight is multiplied as
+// two 16-bit parts, its rounding and what that leaves out, so that o is off by its own rounding only (one
+// part: 1.33 times that, behind 32K tokens in bf16).  That doubles the products of P V, or, where no unit
+// has more than 8 rows (a decode step's own tokens), the second parts take the rows that are free.  (256
+// sequences behind 32K tokens: one part 143 us, products of their own 154, free rows 145.)  At a unit's
+// end the four warps' states are joined in the step's own shared memory, which nothing reads any more,
+// and written as one partial.
 //
 // Measured (d 128, 8 heads, bf16): 32 sequences of up to 16384 tokens (1.1 GB) 168 us a call, 0.97 of a
 // plain copy's bandwidth; 4 behind 128K tokens 93 us, 0.87; 256 sequences of up to 256 tokens 44 us
@@ -87,7 +92,9 @@ __device__ __forceinline__ int page_ids(const PagedArgs &a, const int32_t *row, 
     return id;
 }
 
-template <typename T, int D, int RH>
+// SPARE: no unit has more than 8 rows.  Rows 8 .. 15 of the products then take what rounding the weights
+// of rows 0 .. 7 has left out, in place of products of their own.
+template <typename T, int D, int RH, bool SPARE>
 __global__ void __launch_bounds__(PG_NT, PG_CTAS)
     k_paged(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int wait_first,
             const __grid_constant__ CUtensorMap map) {
@@ -317,6 +324,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                         mx[e] = m;
                         sum[e] *= f[e];
                     }
+                    if (SPARE) f[1] = f[0];
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) {
                         o[n][0] *= f[0];
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                         o[n][3] *= f[1];
                     }
                 }
-                uint32_t pf[4];
+                uint32_t pf[4], pr[4];  // the weights in 16 bits, and what that leaves out
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float m = mx[e] == -INFINITY ? 0.0f : mx[e];  // a row that sees nothing so far
@@ -337,6 +345,12 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                     }
                     pf[e] = T::pack(p[0], p[1]);
                     pf[2 + e] = T::pack(p[2], p[3]);
+                    pr[e] = pack_rest<T>(pf[e], p[0], p[1]);
+                    pr[2 + e] = pack_rest<T>(pf[2 + e], p[2], p[3]);
+                }
+                if (SPARE) {
+                    pf[1] = pr[0];
+                    pf[3] = pr[2];
                 }
                 const int r = w0 + (mi & 1) * 8 + ri;
 #pragma unroll
@@ -350,6 +364,11 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                         T::mma(o[2 * (c0 + c)], pf, b[c][0], b[c][1]);
                         T::mma(o[2 * (c0 + c) + 1], pf, b[c][2], b[c][3]);
                     }
+#pragma unroll
+                    for (int c = 0; c < 4 && !SPARE; ++c) {
+                        T::mma(o[2 * (c0 + c)], pr, b[c][0], b[c][1]);
+                        T::mma(o[2 * (c0 + c) + 1], pr, b[c][2], b[c][3]);
+                    }
                 }
             }
             if (s.flags & PG_LAST) {
@@ -360,6 +379,11 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                     sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
                     sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
                     if (t == 0) *reinterpret_cast<float2 *>(ml + (warp * 16 + g + 8 * e) * 2) = make_float2(mx[e], sum[e]);
+                }
+#pragma unroll
+                for (int n = 0; n < D / 8 && SPARE; ++n) {
+                    o[n][0] += o[n][2];
+                    o[n][1] += o[n][3];
                 }
                 if (!cons_sync()) break;  // and no warp reads the slot's K and V any more
                 float *buf = reinterpret_cast<float *>(st);
@@ -571,17 +595,17 @@ cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long l
 cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype, int d,
                          cudaStream_t s) {
     const int rows = 1 << (l.tt_shift + a.g_shift);
-#define VERKV_PAGED(TT, DT, DD, RR)                                                        \
-    if (dtype == DT && d == DD && rows == 16 * RR) {                                       \
+#define VERKV_PAGED(TT, DT, DD, RR, SP)                                                    \
+    if (dtype == DT && d == DD && rows == 16 * RR && (l.spare != 0) == SP) {               \
         const size_t smem = PagedLayout<DD, RR>::BYTES;                                    \
-        const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD, RR>, smem);        \
+        const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD, RR, SP>, smem);    \
         if (e != cudaSuccess) return e;                                                    \
-        return launch_pdl(k_paged<TT, DD, RR>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
+        return launch_pdl(k_paged<TT, DD, RR, SP>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
     }
-    VERKV_PAGED(PgBf16, VERKV_BF16, 128, 1) VERKV_PAGED(PgBf16, VERKV_BF16, 128, 2)
-    VERKV_PAGED(PgBf16, VERKV_BF16, 64, 1) VERKV_PAGED(PgBf16, VERKV_BF16, 64, 2)
-    VERKV_PAGED(PgF16, VERKV_F16, 128, 1) VERKV_PAGED(PgF16, VERKV_F16, 128, 2)
-    VERKV_PAGED(PgF16, VERKV_F16, 64, 1) VERKV_PAGED(PgF16, VERKV_F16, 64, 2)
+#define VERKV_PAGED_D(TT, DT, DD) VERKV_PAGED(TT, DT, DD, 1, true) VERKV_PAGED(TT, DT, DD, 1, false) VERKV_PAGED(TT, DT, DD, 2, false)
+    VERKV_PAGED_D(PgBf16, VERKV_BF16, 128) VERKV_PAGED_D(PgBf16, VERKV_BF16, 64)
+    VERKV_PAGED_D(PgF16, VERKV_F16, 128) VERKV_PAGED_D(PgF16, VERKV_F16, 64)
+#undef VERKV_PAGED_D
 #undef VERKV_PAGED
     return cudaErrorInvalidValue;
 }

@@ -6,7 +6,8 @@
 // one KV head); it streams 128-token steps of K and V by TMA into a shared-memory ring, and for
 // every step
 //     S = Q K^T   128 x 128, Q and K in shared memory,       float32 in tensor memory
-//     P = 2^(S c - ref), 16 bits, written over S in tensor memory
+//     P = 2^(S c - ref), 16 bits, written over S in tensor memory; with 128 rows in two parts, the
+//         rounded weights and what rounding leaves out, which fill S's place between them
 //     O += P V    128 x d, P in tensor memory, V in shared memory
 // Two such chains run side by side so that one's softmax hides behind the other's products: with
 // 256 rows, the two halves of the rows on the same step; with 128 rows, even and odd steps, joined
@@ -24,6 +25,12 @@
 // maximum less SHIFT, and is raised -- with O scaled in tensor memory -- only when the maximum has
 // risen by more than SLACK since: rarely after the first steps, and no weight passes
 // 2^(SHIFT + SLACK) <= 2^14.  fp16 weights sit 2^8 up, away from its subnormals.
+//
+// Weights in two parts leave o off by its own rounding alone (32K tokens, bf16: 1.64e-3 of its root mean
+// square) at twice the products of P V.  With 128 rows the bytes bound a step and that costs little (8
+// sequences behind 32K tokens 40.5 -> 43.9 us).  With 256 rows the products bound it: 256 sequences behind
+// 32K tokens would go from 143 to 217 us, a prompt of 32768 from 11.7 to 14.0 ms.  There the weights are
+// rounded once, as o is (2.2e-3 in all); the sum they are divided by is not.
 //
 // Measured (8 heads, d 128, bf16; whole calls): 1024 rows a head behind 128K tokens 405 us,
 // 1.36 PFLOP/s, 0.71 of a library matrix product's rate; behind 32K tokens 120 us; 32 rows behind 128K
@@ -67,6 +74,7 @@ struct WideLayout {
     static constexpr int SLOT = HALVES * BOX;           // K or V of a step; also a tile of Q
     static constexpr int NS = D == 128 ? (TILES == 2 ? 5 : 6) : 10;
     static constexpr int R = TILES * 128;
+    static constexpr bool REST = TILES == 1;            // weights in two parts (see above)
     static constexpr int Q = 0;
     static constexpr int RING = TILES * SLOT;
     static constexpr int ML = RING + NS * SLOT;                          // float [2][128][2]
@@ -342,16 +350,25 @@ __global__ void __launch_bounds__(PW_NT, 1)
                     // The first half of P's tokens, while the softmax writes the second.
                     if (valid > PAGED_WIDE_TILE - 16) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) mma_ts(ot, pt + x * 8, vd + x * 128, IO, add || x > 0, it);
+                        for (int x = 0; x < 4; ++x) {
+                            mma_ts(ot, pt + x * 8, vd + x * 128, IO, add || x > 0, it);
+                            if (LY::REST) mma_ts(ot, pt + 64 + x * 8, vd + x * 128, IO, true, it);
+                        }
                         if (!(go = await(&p_full[i], ns[i]))) break;
                         tcgen05_after_sync();
 #pragma unroll
-                        for (int x = 4; x < 8; ++x) mma_ts(ot, pt + x * 8, vd + x * 128, IO, true, it);
+                        for (int x = 4; x < 8; ++x) {
+                            mma_ts(ot, pt + x * 8, vd + x * 128, IO, true, it);
+                            if (LY::REST) mma_ts(ot, pt + 64 + x * 8, vd + x * 128, IO, true, it);
+                        }
                     } else {
                         if (!(go = await(&p_full[i], ns[i]))) break;
                         tcgen05_after_sync();
 #pragma unroll 1
-                        for (int x = 0; x < (valid + 15) / 16; ++x) mma_ts(ot, pt + x * 8, vd + x * 128, IO, add || x > 0, it);
+                        for (int x = 0; x < (valid + 15) / 16; ++x) {
+                            mma_ts(ot, pt + x * 8, vd + x * 128, IO, add || x > 0, it);
+                            if (LY::REST) mma_ts(ot, pt + 64 + x * 8, vd + x * 128, IO, true, it);
+                        }
                     }
                     ++ns[i];
                     if (more) do_s(n + 2);
@@ -444,7 +461,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                     unsigned long long part[2] = {0ull, 0ull};  // pairs of floats
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t p[32];
+                        uint32_t p[32], rest[32];
 #pragma unroll
                         for (int x = 0; x < 32; ++x) {
                             float u = __uint_as_float(s[64 * h + 2 * x]), v = __uint_as_float(s[64 * h + 2 * x + 1]);
@@ -452,9 +469,11 @@ __global__ void __launch_bounds__(PW_NT, 1)
                             u = exp2_fast(u);
                             v = exp2_fast(v);
                             p[x] = T::pack(u, v);
+                            if (LY::REST) rest[x] = pack_rest<T>(p[x], u, v);
                             add2(part[x & 1], u, v);
                         }
                         tmem_st32(ts + 32 * h, p);
+                        if (LY::REST) tmem_st32(ts + 64 + 32 * h, rest);
                         tmem_wait_st();
                         if (h == 0) {
                             tcgen05_before_sync();

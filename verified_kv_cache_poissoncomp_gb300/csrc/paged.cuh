@@ -23,6 +23,8 @@
 #include <stdint.h>
 
 #ifdef __CUDACC__
+#include <cuda_fp16.h>
+
 #include "verkv_common.cuh"
 #endif
 #include "verkv_internal.h"
@@ -62,6 +64,7 @@ struct PagedLine {
     int ctas;                   // CTAs launched
     int slots;                  // partial slots there is room for
     int tall;                   // (host: tiles of 256 rows)
+    int spare;                  // (host: no unit has more than 8 rows)
     double cost, units;         // (host: us of one SM; about how many units)
     int2 *rec;                  // {per, room}, then {work before, units before} of each segment with work; per 0: a bad segment, no work
     int grouped;                // 0: part_o [slots][tt * G][d]; 1: [slots][tt * G / 4][d / 4][4 rows][4]
@@ -320,6 +323,7 @@ struct PgBf16 {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
         return y;
     }
+    static __device__ __forceinline__ float2 unpack(uint32_t x) { return make_float2(bf16lo(x), bf16hi(x)); }
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -335,6 +339,7 @@ struct PgF16 {
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
         return y;
     }
+    static __device__ __forceinline__ float2 unpack(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -343,6 +348,18 @@ struct PgF16 {
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 };
+// What rounding a pair of weights to 16 bits has left out of it, in 16 bits of its own: together they hold
+// a weight to within 2^-16 (bf16) or 2^-22 (fp16) of itself.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_rest(uint32_t packed, float lo, float hi) {
+    const float2 f = T::unpack(packed);
+    unsigned long long v, w;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(-f.x), "f"(-f.y));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    return T::pack(lo, hi);
+}
 // 2^x to within 2 units of the last place, 0 for -infinity.
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;

@@ -1240,6 +1240,9 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         lines[1].tile_shift = log2_of(PAGED_WIDE_TILE);
         lines[1].grouped = 1;
         lines[1].tall = tall;
+        // Known here: one query a sequence where q_start is not given, and all of them behind a single prefix.
+        lines[0].spare = (!lines[0].with[0] || (groups == 1 && (int64_t)q_tokens * sh.q_per_kv <= 8)) &&
+                         (!lines[0].with[1] || !q_start);
         bool ok = true;
         if (many) ok &= paged_line(ctx, a, lines[1], tall ? 256 : 128, std::min(ctx->sms, PAGED_WIDE_CTAS), (unsigned char *)workspace, off);
         const int64_t rows_few = std::max(lines[0].with[0] ? rows_prefix : 0, lines[0].with[1] ? rows_own : 0);
