@@ -482,9 +482,14 @@ size_t verkv_paged_workspace_size(const verkv_shape *shape, int32_t seqs, int32_
  *                            into one CTA (clusters of 1 and 4 do by default, when at most 512
  *                            remain) but runs its histogram passes to the end, for a bitwise
  *                            comparison of the two; 1 restores the default.
+ *   VERKV_INJECT_PAGED_STALL value >= 1000: in the next verkv_paged_attend the first CTA of each
+ *                            attention kernel arms its first copy barrier for copies it never
+ *                            issues, and the kernels' bounded waits give up after `value` ns: they
+ *                            latch VERKV_ETIMEOUT, wait for the copies in flight and return; the
+ *                            call's outputs are not valid, and the context stays usable.  One call.
  * Returns VERKV_EINVAL for an unknown `what` or a value out of range. */
 enum { VERKV_INJECT_COPY_FAIL = 1, VERKV_INJECT_BETA_MAXIT = 2, VERKV_INJECT_SCORE_STALL = 3,
-       VERKV_INJECT_SELECT_GATHER = 4 };
+       VERKV_INJECT_SELECT_GATHER = 4, VERKV_INJECT_PAGED_STALL = 5 };
 verkv_status verkv_test_inject(verkv_ctx *ctx, int what, int64_t value);
 
 /* Measurement.  Every kernel launch is counted per kernel; with profiling enabled each launch is

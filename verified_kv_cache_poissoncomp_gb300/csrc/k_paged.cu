@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
 #pragma unroll 1
             for (int t = cur.t0; t < cur.t1; ++t, ++j) {
                 const int k = j % NS;
-                if (j >= NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort));
+                if (j >= NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort, a.wait_ns));
                 if (!go) break;
                 const int tok0 = t * PAGED_TILE, valid = min(PAGED_TILE, cur.vis - tok0);
                 const int pages = (valid + box - 1) / box, p0 = tok0 >> a.page_shift;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                     // The queries' slot: the piece before the last one has begun to be worked on.  (Of a step
                     // NS back that is known, and its barrier may be phases ahead.)
                     const int b = begun[0];
-                    if (b >= 0 && b > j - NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[b % NS], (uint32_t)((b / NS) & 1), abort));
+                    if (b >= 0 && b > j - NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[b % NS], (uint32_t)((b / NS) & 1), abort, a.wait_ns));
                     if (!go) break;
                     begun[0] = begun[1];
                     begun[1] = j;
@@ -192,14 +192,15 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
                 }
                 __syncwarp();
                 const int id = __shfl_sync(0xFFFFFFFFu, cur.ids, (p0 + lane - cur.ids0) & 31);
-                if (lane < pages) {
+                const bool stalled = a.stall && blockIdx.x == 0 && j == 0;
+                if (lane < pages && !stalled) {
                     // a page of more than one step is read at the step's offset in it
                     const int y = (((id * a.hkv + cur.head) << a.page_shift) + ((tok0 + lane * box) & ((1 << a.page_shift) - 1)));
                     unsigned char *st = pg_smem + (size_t)k * LY::STAGE + lane * box * 128;
 #pragma unroll
                     for (int b = 0; b < 2 * LY::HALVES; ++b) tma_load_2d(st + b * LY::BOX, &map, b * 64, y, &full[k]);
                 }
-                if (first && lane < cur.rows) {
+                if (first && lane < cur.rows && !stalled) {
                     const int jj = lane >> a.g_shift, hh = (cur.head << a.g_shift) + lane - (jj << a.g_shift);
                     bulk_g2s(pg_smem + LY::Q + (np % LY::QN * R + lane) * LY::QROW, a.q + (cur.q0 + jj) * a.q_ts + hh * a.q_hs, 2 * D, &full[k]);
                 }
@@ -210,18 +211,21 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         }
         if (go) {  // tell the consumers that the run is over
             const int k = j % NS;
-            if (j >= NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort));
+            if (j >= NS) go = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&empty[k], (uint32_t)((j / NS - 1) & 1), abort, a.wait_ns));
             if (go && lane == 0) {
                 desc[k].flags = PG_END;
                 mbar_arrive(&full[k]);
             }
         }
-        if (!go && lane == 0) {
-            // A wait ran out.  Let the copies of this CTA land before it exits: the steps j - NS ..
-            // j - 1 are the ones that may be in flight.
-            *abort = 1;
-            raise_error(a.err, ERR_TIMEOUT);
-            for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1));
+        if (lane == 0) {
+            if (!go) {  // a wait ran out
+                *abort = 1;
+                raise_error(a.err, ERR_TIMEOUT);
+            }
+            // The copies in flight land before the CTA gives its shared memory back, also where another
+            // warp's wait ran out after the last of them was issued.  They are of the last NS steps; the
+            // place of the first of those holds the end of the run by now, if that has been told.
+            for (int i = max(0, j - NS + (go ? 1 : 0)); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1), a.wait_ns);
         }
         __syncwarp();
     } else {
@@ -236,13 +240,18 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         auto cons_sync = [&]() -> bool {
             __syncwarp();
             if (lane == 0) mbar_arrive(join);
-            const bool ok = mbar_wait_or_abort(join, (uint32_t)(joins & 1), abort);
+            const bool ok = mbar_wait_or_abort(join, (uint32_t)(joins & 1), abort, a.wait_ns);
             ++joins;
-            return __all_sync(0xFFFFFFFFu, ok);
+            if (__all_sync(0xFFFFFFFFu, ok)) return true;
+            if (lane == 0) {
+                *abort = 1;
+                raise_error(a.err, ERR_TIMEOUT);
+            }
+            return false;
         };
         for (int j = 0;; ++j) {
             const int k = j % NS;
-            const bool ok = mbar_wait_or_abort(&full[k], (uint32_t)((j / NS) & 1), abort);
+            const bool ok = mbar_wait_or_abort(&full[k], (uint32_t)((j / NS) & 1), abort, a.wait_ns);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 if (lane == 0) {
                     *abort = 1;

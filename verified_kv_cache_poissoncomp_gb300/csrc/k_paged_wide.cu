@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     const uint32_t tm = *tmem_at;
     // S (and P over it) of chain i in columns 128 i .., O in 256 + 128 i ..
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = paged_wait(smem_addr(bar), parity, abort);
+        const bool ok = paged_wait(smem_addr(bar), parity, abort, a.wait_ns);
         if (__all_sync(0xFFFFFFFFu, ok)) return true;
         if (lane == 0) {
             *abort = 1;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                     mbar_expect_tx(&full[k], (uint32_t)(n * box * 2 * D));
                 }
                 __syncwarp();
-                if (lane < n) {
+                if (lane < n && !(a.stall && blockIdx.x == 0 && j == 0)) {
                     unsigned char *st = pw_smem + LY::RING + (size_t)k * LY::SLOT + lane * box * 128;
 #pragma unroll
                     for (int b = 0; b < LY::HALVES; ++b)
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
         if (lane == 0) {
             // The copies in flight land here even where another warp's wait ran out: they are the last NS
             // slots issued.
-            for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1));
+            for (int i = max(0, j - NS); i < j; ++i) mbar_wait_bounded(&full[i % NS], (uint32_t)((i / NS) & 1), a.wait_ns);
         }
         __syncwarp();
     } else if (warp == PW_MMA) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
             constexpr uint32_t IS = mma_desc(128, 128, W::BF, false), IO = mma_desc(128, D, W::BF, true);
             using Order = WideOrder<TILES>;
             auto await = [&](uint64_t *bar, uint32_t parity) -> bool {
-                if (__all_sync(0xFFFFFFFFu, paged_wait(smem_addr(bar), parity, abort))) return true;
+                if (__all_sync(0xFFFFFFFFu, paged_wait(smem_addr(bar), parity, abort, a.wait_ns))) return true;
                 *abort = 1;
                 raise_error(a.err, ERR_TIMEOUT);
                 return false;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
             }
             // Nothing is in flight when the CTA gives its tensor memory back.
             tcgen05_commit(drain, it);
-            if (!mbar_wait_bounded(drain, 0u)) raise_error(a.err, ERR_TIMEOUT);
+            if (!mbar_wait_bounded(drain, 0u, a.wait_ns)) raise_error(a.err, ERR_TIMEOUT);
         }
         __syncwarp();
     } else {

@@ -83,6 +83,8 @@ struct PagedArgs {
     const float *prior_o, *prior_lse;
     uint16_t *o;
     float *lse;
+    unsigned long long wait_ns;  // limit of the kernels' waits
+    int stall;                   // injected: the first copies of the first CTA are not issued
 };
 
 constexpr int PAGED_MAX_CTAS = 304;   // of k_paged: two an SM
@@ -90,6 +92,7 @@ constexpr int PAGED_WIDE_CTAS = 152;  // of k_paged_wide
 constexpr int PAGED_TILE = 64;        // tokens of a step of k_paged
 constexpr int PAGED_ROWS = 32;        // most rows of its units (16 or 32)
 constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
+constexpr unsigned long long PAGED_WAIT_NS = 1000000000ull;  // 1 s: limit of a wait
 constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
 constexpr int PAGED_SLACK = 2;        // steps a run may be longer for units of whole runs
 
@@ -380,18 +383,18 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
 // Wait for phase `parity` of the barrier at shared address `bar`; false when *abort is set or the time
 // is up.  The first poll is in line and the rest is a call: a warp that issues products or copies runs
 // between others that fill the instruction cache, and pays for each line of code it passes.
-static __device__ __noinline__ bool paged_wait_long(uint32_t bar, uint32_t parity, volatile int *abort) {
+static __device__ __noinline__ bool paged_wait_long(uint32_t bar, uint32_t parity, volatile int *abort, unsigned long long limit_ns) {
     unsigned long long t0 = 0;
     for (;;) {
         for (int i = 0; i < 16; ++i)
             if (mbar_poll(bar, parity)) return true;
         const unsigned long long t = globaltimer_ns();
         if (t0 == 0) t0 = t;
-        if (*abort || t - t0 > TMA_WAIT_NS) return false;
+        if (*abort || t - t0 > limit_ns) return false;
     }
 }
-__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return mbar_poll(bar, parity) || paged_wait_long(bar, parity, abort);
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned long long limit_ns) {
+    return mbar_poll(bar, parity) || paged_wait_long(bar, parity, abort, limit_ns);
 }
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {

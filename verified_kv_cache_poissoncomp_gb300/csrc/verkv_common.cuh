@@ -284,11 +284,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
 }
 
 // The same wait, which also gives up as soon as *abort is set (by another thread that timed out).
-__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                                   unsigned long long limit_ns = TMA_WAIT_NS) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity))
-        if (*abort || globaltimer_ns() - t0 > TMA_WAIT_NS) return false;
+        if (*abort || globaltimer_ns() - t0 > limit_ns) return false;
     return true;
 }
 
