@@ -487,9 +487,11 @@ size_t verkv_paged_workspace_size(const verkv_shape *shape, int32_t seqs, int32_
  *                            issues, and the kernels' bounded waits give up after `value` ns: they
  *                            latch VERKV_ETIMEOUT, wait for the copies in flight and return; the
  *                            call's outputs are not valid, and the context stays usable.  One call.
+ *   VERKV_INJECT_PAGED_LIMIT value >= 1000: the same limit alone, for the next verkv_paged_attend.
  * Returns VERKV_EINVAL for an unknown `what` or a value out of range. */
 enum { VERKV_INJECT_COPY_FAIL = 1, VERKV_INJECT_BETA_MAXIT = 2, VERKV_INJECT_SCORE_STALL = 3,
-       VERKV_INJECT_SELECT_GATHER = 4, VERKV_INJECT_PAGED_STALL = 5 };
+       VERKV_INJECT_SELECT_GATHER = 4, VERKV_INJECT_PAGED_STALL = 5,
+       VERKV_INJECT_PAGED_LIMIT = 6 };
 verkv_status verkv_test_inject(verkv_ctx *ctx, int what, int64_t value);
 
 /* Measurement.  Every kernel launch is counted per kernel; with profiling enabled each launch is

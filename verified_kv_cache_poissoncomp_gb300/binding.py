@@ -40,7 +40,7 @@ EXPORTED = ["verkv_sketch_bytes", "verkv_workspace_size", "verkv_create", "verkv
             "verkv_set_sequence_offset", "verkv_rope_turns", "verkv_norm_rotate",
             "verkv_paged_append", "verkv_paged_attend", "verkv_paged_workspace_size"]
 VERKV_INJECT_COPY_FAIL, VERKV_INJECT_BETA_MAXIT, VERKV_INJECT_SCORE_STALL = 1, 2, 3
-VERKV_INJECT_SELECT_GATHER, VERKV_INJECT_PAGED_STALL = 4, 5
+VERKV_INJECT_SELECT_GATHER, VERKV_INJECT_PAGED_STALL, VERKV_INJECT_PAGED_LIMIT = 4, 5, 6
 # kernel ids (include/verkv.h), in launch order
 (VERKV_K_PC_SOLVE, VERKV_K_PC_GATHER, VERKV_K_SKETCH, VERKV_K_SCORE, VERKV_K_CERTIFY,
  VERKV_K_PARTIAL_PIVOTAL, VERKV_K_FETCH_HOST, VERKV_K_PARTIAL_STAGED, VERKV_K_MERGE,

@@ -116,15 +116,18 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort = 0;
     }
+    if (warp == PG_CONS) {
+        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+        // Before the CTA's barrier: no wait's limit counts what the kernels ahead still take.  (The other
+        // kernel of the call lets this one start when it has waited itself.)
+        if (wait_first) pdl_wait();
+        pdl_trigger();
+    }
     __syncthreads();
 
     if (warp == PG_CONS) {
-        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
         const int box = min(1 << a.page_shift, PAGED_TILE);  // tokens of a page in one step
         PagedWalk<false> wk;
-        // (the other kernel of the call lets this one start when it has waited itself)
-        if (wait_first) pdl_wait();
-        pdl_trigger();
         // (the queries' place holds nothing yet)
         wk.start(a, l, blockIdx.x, reinterpret_cast<int2 *>(pg_smem + LY::Q), LY::QN * R * LY::QROW / 8);
         fence_proxy_async_smem();  // these accesses before the queries' copies to the same place

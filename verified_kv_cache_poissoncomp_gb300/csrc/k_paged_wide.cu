@@ -167,6 +167,12 @@ __global__ void __launch_bounds__(PW_NT, 1)
         *abort = 0;
     }
     if (warp == PW_MMA) tmem_alloc(tmem_at, 512);
+    if (warp == PW_COPY) {
+        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+        // Before the CTA's barrier: no wait's limit counts what the kernels ahead still take.
+        if (wait_first) pdl_wait();
+        pdl_trigger();
+    }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -183,10 +189,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     };
 
     if (warp == PW_COPY) {
-        if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
         // The other warps touch the caller's data only after the first piece that this one announces.
-        if (wait_first) pdl_wait();
-        pdl_trigger();
         // (the chains' states have no use for their place yet)
         PagedWalk<true> wk;
         wk.start(a, l, blockIdx.x, reinterpret_cast<int2 *>(ml), 2 * 128);

@@ -224,7 +224,8 @@ struct verkv_ctx {
     int sel_gather = 1;              // the select's gathered finish (clusters of 1 and 4)
     int seq0 = 0;                    // Philox sequence index of this context's first sequence
     int64_t score_stall_ns = 0;      // > 0: the next attend's scoring kernel stalls one stage
-    int64_t paged_stall_ns = 0;      // > 0: the next paged attention's kernels stall one step each
+    int64_t paged_wait_ns = 0;       // > 0: limit of the next paged attention's waits
+    bool paged_stall = false;        // and its kernels stall one step each
     // Measurement
     int64_t launches[VERKV_K_COUNT] = {};
     bool prof_on = false;
@@ -1223,10 +1224,11 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
     a.o = (uint16_t *)o_out;
     a.lse = lse_out;
     a.wait_ns = PAGED_WAIT_NS;
-    if (ctx->paged_stall_ns > 0) {  // injected: stalled copies, a short wait limit
-        a.wait_ns = (unsigned long long)ctx->paged_stall_ns;
-        a.stall = 1;
-        ctx->paged_stall_ns = 0;
+    if (ctx->paged_wait_ns > 0) {  // injected: a short wait limit, stalled copies
+        a.wait_ns = (unsigned long long)ctx->paged_wait_ns;
+        a.stall = ctx->paged_stall;
+        ctx->paged_wait_ns = 0;
+        ctx->paged_stall = false;
     }
 
     PagedLines both{};
@@ -1297,8 +1299,10 @@ verkv_status verkv_test_inject(verkv_ctx *ctx, int what, int64_t value) {
             ctx->score_stall_ns = value;
             return VERKV_OK;
         case VERKV_INJECT_PAGED_STALL:
+        case VERKV_INJECT_PAGED_LIMIT:
             if (value < 1000 || value > 1000000000LL) break;
-            ctx->paged_stall_ns = value;
+            ctx->paged_wait_ns = value;
+            ctx->paged_stall = what == VERKV_INJECT_PAGED_STALL;
             return VERKV_OK;
         case VERKV_INJECT_SELECT_GATHER:
             if (value < 0 || value > 1) break;
