@@ -96,7 +96,7 @@ __device__ __forceinline__ int page_ids(const PagedArgs &a, const int32_t *row, 
 // of rows 0 .. 7 has left out, in place of products of their own.
 template <typename T, int D, int RH, bool SPARE>
 __global__ void __launch_bounds__(PG_NT, PG_CTAS)
-    k_paged(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int wait_first,
+    k_paged(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int second,
             const __grid_constant__ CUtensorMap map) {
     using LY = PagedLayout<D, RH>;
     constexpr int KS = D / 16, NS = LY::NS, R = LY::R;
@@ -118,10 +118,8 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
     }
     if (warp == PG_CONS) {
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
-        // Before the CTA's barrier: no wait's limit counts what the kernels ahead still take.  (The other
-        // kernel of the call lets this one start when it has waited itself.)
-        if (wait_first) pdl_wait();
-        pdl_trigger();
+        // Before the CTA's barrier: no wait's limit counts what the kernels ahead still take.
+        paged_begin(a, second != 0);
     }
     __syncthreads();
 
@@ -466,6 +464,7 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
     __shared__ float states[PM_NT / 32][D + 2];
     pdl_wait();
     pdl_trigger();
+    if (a.ready && blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0ull;  // (see paged_begin)
     const int warp = threadIdx.x >> 5, wi = warp % WPR;  // of the row's warps
     const long long row = (long long)blockIdx.x * (PM_NT / 32 / WPR) + warp / WPR;
     if (row >= (long long)a.q_tokens * hq) return;
@@ -604,7 +603,7 @@ cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long l
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype, int d,
+cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorMap &map, bool second, int dtype, int d,
                          cudaStream_t s) {
     const int rows = 1 << (l.tt_shift + a.g_shift);
 #define VERKV_PAGED(TT, DT, DD, RR, SP)                                                    \
@@ -612,7 +611,7 @@ cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorM
         const size_t smem = PagedLayout<DD, RR>::BYTES;                                    \
         const cudaError_t e = ensure_smem((const void *)k_paged<TT, DD, RR, SP>, smem);    \
         if (e != cudaSuccess) return e;                                                    \
-        return launch_pdl(k_paged<TT, DD, RR, SP>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
+        return launch_pdl(k_paged<TT, DD, RR, SP>, dim3(l.ctas), dim3(PG_NT), smem, s, a, l, second ? 1 : 0, map); \
     }
 #define VERKV_PAGED_D(TT, DT, DD) VERKV_PAGED(TT, DT, DD, 1, true) VERKV_PAGED(TT, DT, DD, 1, false) VERKV_PAGED(TT, DT, DD, 2, false)
     VERKV_PAGED_D(PgBf16, VERKV_BF16, 128) VERKV_PAGED_D(PgBf16, VERKV_BF16, 64)

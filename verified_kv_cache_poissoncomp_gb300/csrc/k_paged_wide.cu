@@ -133,7 +133,7 @@ __device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_fl
 
 template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(PW_NT, 1)
-    k_paged_wide(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int wait_first,
+    k_paged_wide(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLine l, const int second,
                  const __grid_constant__ CUtensorMap map) {
     using LY = WideLayout<D, TILES>;
     using W = Weights<T>;
@@ -170,8 +170,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
     if (warp == PW_COPY) {
         if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
         // Before the CTA's barrier: no wait's limit counts what the kernels ahead still take.
-        if (wait_first) pdl_wait();
-        pdl_trigger();
+        paged_begin(a, second != 0);
     }
     tcgen05_before_sync();
     __syncthreads();
@@ -567,7 +566,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
 
 }  // namespace
 
-cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const CUtensorMap &map, bool wait_first, int dtype,
+cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const CUtensorMap &map, bool second, int dtype,
                               int d, cudaStream_t s) {
     PagedArgs a = args;
     // a scale that rounds to 0 would make the masked logits' -infinity not a number
@@ -578,7 +577,7 @@ cudaError_t launch_paged_wide(const PagedArgs &args, const PagedLine &l, const C
         const size_t smem = WideLayout<DD, NN>::BYTES;                                          \
         const cudaError_t e = ensure_smem((const void *)k_paged_wide<TT, DD, NN>, smem);        \
         if (e != cudaSuccess) return e;                                                         \
-        return launch_pdl(k_paged_wide<TT, DD, NN>, dim3(l.ctas), dim3(PW_NT), smem, s, a, l, wait_first ? 1 : 0, map); \
+        return launch_pdl(k_paged_wide<TT, DD, NN>, dim3(l.ctas), dim3(PW_NT), smem, s, a, l, second ? 1 : 0, map); \
     }
     VERKV_WIDE(PgBf16, VERKV_BF16, 128, 1) VERKV_WIDE(PgBf16, VERKV_BF16, 128, 2)
     VERKV_WIDE(PgBf16, VERKV_BF16, 64, 1) VERKV_WIDE(PgBf16, VERKV_BF16, 64, 2)

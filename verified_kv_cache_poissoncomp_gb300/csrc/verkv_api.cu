@@ -454,7 +454,7 @@ bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_
 size_t paged_workspace(const verkv_shape &sh, int64_t seqs, int64_t groups, int64_t q_tokens) {
     const size_t rec = align256((size_t)(1 + seqs + groups) * 8) * PAGED_LINES;
     const size_t rows = (size_t)paged_rows_bound(sh.kv_heads, sh.q_per_kv, seqs, groups, q_tokens);
-    return rec + rows * (size_t)(sh.head_dim + 2) * 4 + PAGED_LINES * 512;
+    return 256 + rec + rows * (size_t)(sh.head_dim + 2) * 4 + PAGED_LINES * 512;
 }
 
 // Fills in a line over the given segments, taking its buffers from the workspace at `off`; false if
@@ -1233,7 +1233,7 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
 
     PagedLines both{};
     PagedLine *lines = both.l;
-    size_t off = 0;
+    size_t off = 256;  // (the first word: PagedArgs::ready)
     if (a.level[0].rows || a.level[1].rows) {
         // Each level by the rows of its segments; the two lines' launches need not wait for one another.
         const int64_t rows_prefix = a.level[0].rows ? paged_rows(q_tokens, a.level[0].rows, sh.q_per_kv) : 0;
@@ -1266,14 +1266,16 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
         // Side by side, the longer one begins first; one after the other, k_paged, whose start is the longer
         // one with many sequences, begins while the kernel ahead of the call still runs.
         const bool beside = few && many && paged_share(lines[1], lines[0], ctx->sms);
+        // (launches that are timed one by one wait for one another)
+        if (few && many && !ctx->prof_on) a.ready = (unsigned long long *)workspace;
         for (int turn = 0; turn < 2; ++turn) {
             const bool wide = (turn == 0) == (beside || !few);
             if (!(wide ? many : few)) continue;
-            const bool wait_first = turn == 0 || !few || !many || ctx->prof_on;
+            const bool second = turn == 1 && a.ready;
             VERKV_CUDA(make_map(wide ? PAGED_WIDE_TILE : PAGED_TILE), "tensor map of the pages");
             VERKV_CUDA(tracked(ctx, wide ? VERKV_K_PAGED_WIDE : VERKV_K_PAGED, ctx->main, [&] {
-                           return wide ? launch_paged_wide(a, lines[1], map, wait_first, pages->dtype, sh.head_dim, ctx->main)
-                                       : launch_paged(a, lines[0], map, wait_first, pages->dtype, sh.head_dim, ctx->main);
+                           return wide ? launch_paged_wide(a, lines[1], map, second, pages->dtype, sh.head_dim, ctx->main)
+                                       : launch_paged(a, lines[0], map, second, pages->dtype, sh.head_dim, ctx->main);
                        }), wide ? "k_paged_wide" : "k_paged");
         }
     }
