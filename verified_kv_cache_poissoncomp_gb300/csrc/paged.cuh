@@ -96,6 +96,7 @@ constexpr int PAGED_WIDE_TILE = 128;  // and of k_paged_wide
 constexpr unsigned long long PAGED_WAIT_NS = 1000000000ull;  // 1 s: limit of a wait
 constexpr int PAGED_LINES = 2;        // launches of a call: one of each kernel at most
 constexpr int PAGED_SLACK = 2;        // steps a run may be longer for units of whole runs
+constexpr int PAGED_ROOMS_MOST = 1 << 21;  // steps of a line whose units may get whole runs
 
 cudaError_t paged_tensor_map(CUtensorMap *map, const void *kv, int dtype, long long rows, int d, int box_rows);
 // second: the launch before it on the stream is this call's other kernel, which it need not wait for to
@@ -243,9 +244,9 @@ struct PagedWalk {
         total = __reduce_add_sync(0xFFFFFFFFu, total) * a.hkv;
         bad = __any_sync(0xFFFFFFFFu, bad);
         int per = bad ? 0 : (int)max(1u, ((unsigned)total + l.ctas - 1) / (unsigned)l.ctas);
-        if (ROOMS && n <= 32 && per > 0 && per < 1 << 20) {
+        if (ROOMS && n <= 32 && per > 0 && total < PAGED_ROOMS_MOST) {
             // A lane a segment.  (Quotients by the fast reciprocal, whose error of two units of the last place
-            // is less than the halves added here; p is put right if not.)
+            // is less than the halves added here, up to PAGED_ROOMS_MOST steps; p is put right if not.)
             const int2 g = lane < n ? cache[lane] : make_int2(0, 0);
             const int units = __reduce_add_sync(0xFFFFFFFFu, g.y) * a.hkv;
             if (units <= l.ctas && total > 0) {
