@@ -456,6 +456,22 @@ __device__ __forceinline__ int last_at_most(const int32_t *start, int n, int x) 
 
 constexpr int PM_NT = 128;
 
+// start[0 .. n] ascends from 0 to `end`, or the call is reported; all threads of the grid.
+__device__ __forceinline__ void check_starts(const PagedArgs &a, const int32_t *start, int n, int end) {
+    for (int i = blockIdx.x * PM_NT + threadIdx.x; i <= n; i += gridDim.x * PM_NT) {
+        const int x = start[i];
+        if (i == n ? x != end : x > start[i + 1] || (i == 0 && x != 0)) raise_error(a.err, ERR_PAGE);
+    }
+}
+// (A call: most launches have nothing of the kind, and pay for the code they pass.)
+static __device__ __noinline__ void check_unseen(const PagedArgs &a) {
+    if (a.check_q_start) check_starts(a, a.q_start, a.seqs, a.q_tokens);
+    if (a.check_group_start) check_starts(a, a.group_start, a.zero_rows[0], a.seqs);
+    for (int x = 0; x < 2; ++x)
+        for (int i = blockIdx.x * PM_NT + threadIdx.x; i < a.zero_rows[x]; i += gridDim.x * PM_NT)
+            if (a.zero_length[x][i] != 0) raise_error(a.err, ERR_PAGE);
+}
+
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ PagedArgs a, const __grid_constant__ PagedLines lines) {
     constexpr int V = D / 32;  // channels a lane holds
@@ -465,6 +481,7 @@ __global__ void __launch_bounds__(PM_NT) k_paged_merge(const __grid_constant__ P
     pdl_wait();
     pdl_trigger();
     if (a.ready && blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0ull;  // (see paged_begin)
+    if (a.unseen) check_unseen(a);
     const int warp = threadIdx.x >> 5, wi = warp % WPR;  // of the row's warps
     const long long row = (long long)blockIdx.x * (PM_NT / 32 / WPR) + warp / WPR;
     if (row >= (long long)a.q_tokens * hq) return;

@@ -77,6 +77,10 @@ struct PagedArgs {
     long long q_ts, q_hs;
     const int32_t *q_start, *group_start;
     PagedLevel level[2];  // of the prefixes, and of the sequences' own tokens
+    // What no segment looks at: lengths of levels whose bound is 0, and starts of a level that is absent.
+    const int32_t *zero_length[2];
+    int zero_rows[2];
+    bool check_q_start, check_group_start, unseen;  // unseen: any of these
     int seqs, q_tokens, hkv, g_shift, page_shift, num_pages;  // q_per_kv = 2^g_shift
     float scale_log2;  // logits are taken in units of log 2
     uint32_t *err;

@@ -1211,6 +1211,16 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
     };
     a.level[0] = level(prefix && prefix->max_length > 0 ? prefix : nullptr);
     a.level[1] = level(own && own->max_length > 0 ? own : nullptr);
+    // What the segments of the levels do not look at, the merge does.
+    const verkv_span *const spans[2] = {prefix, own};
+    for (int x = 0; x < 2; ++x) {
+        if (!spans[x] || spans[x]->max_length > 0) continue;
+        a.zero_length[x] = spans[x]->length;
+        a.zero_rows[x] = spans[x]->rows;
+    }
+    a.check_q_start = q_start && !a.level[1].rows;
+    a.check_group_start = group_start && !a.level[0].rows;
+    a.unseen = a.check_q_start || a.check_group_start || a.zero_rows[0] || a.zero_rows[1];
     a.seqs = seqs;
     a.q_tokens = q_tokens;
     a.hkv = sh.kv_heads;
