@@ -439,13 +439,20 @@ int64_t paged_rows(int64_t q_tokens, int64_t segments, int G) { return (q_tokens
 bool paged_wide_prefix(int64_t rows) { return rows > PAGED_ROWS / 2; }
 bool paged_wide_own(int64_t rows) { return rows > PAGED_ROWS; }
 
-// Upper bound of the partial rows of any call for up to these sizes.  Of one level: its queries'
-// rows q G, at most one ragged row tile a segment, and one slot a CTA.  A level in tiles of 128 rows
-// has more than 16 rows a segment on average, one in tiles of 256 more than 128: its ragged tiles add
-// at most 128 / 16 q G.
+// Upper bound of the partial rows of one level of `segs` segments, for one head and without the slot a CTA:
+// its queries' rows q G, and a ragged row tile a segment.  Tiles have up to 32 rows, or 128 where segments
+// have more than 16 rows on average (there are fewer than q G / 16 then), or 256 where more than 128.
+int64_t paged_level_rows(int64_t G, int64_t segs, int64_t q_tokens) {
+    const int64_t rows = q_tokens * G;
+    return rows + std::max(PAGED_ROWS * segs, std::max(std::min(128 * segs, 8 * rows), std::min(256 * segs, 2 * rows)));
+}
+// Of any call for up to these sizes: both levels, or without prefixes only the sequences' own, and the slots
+// of its launches' CTAs.
 int64_t paged_rows_bound(int64_t hkv, int64_t G, int64_t seqs, int64_t groups, int64_t q_tokens) {
-    return hkv * (2 * 9 * q_tokens * G + PAGED_ROWS * (seqs + groups)) + (int64_t)PAGED_MAX_CTAS * PAGED_ROWS +
-           (int64_t)PAGED_WIDE_CTAS * 256;
+    const int64_t rows = q_tokens * G, few = (int64_t)PAGED_MAX_CTAS * PAGED_ROWS;
+    const int64_t wide = (int64_t)PAGED_WIDE_CTAS * (rows > 128 ? 256 : rows > PAGED_ROWS / 2 ? 128 : 0);
+    if (groups == 0) return hkv * paged_level_rows(G, seqs, q_tokens) + std::max(few, wide);
+    return hkv * (paged_level_rows(G, seqs, q_tokens) + paged_level_rows(G, groups, q_tokens)) + few + wide;
 }
 bool paged_sizes_ok(int64_t seqs, int64_t groups, int64_t q_tokens, const verkv_shape &sh) {
     return seqs >= 0 && groups >= 0 && q_tokens >= 0 && seqs <= PAGED_MAX_SEGMENTS && groups <= PAGED_MAX_SEGMENTS &&
