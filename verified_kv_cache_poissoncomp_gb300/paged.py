@@ -16,6 +16,8 @@ from . import binding as B
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
+
 _DTYPES = {torch.bfloat16: B.VERKV_BF16, torch.float16: B.VERKV_F16}
 
 
@@ -76,10 +78,10 @@ class PagedKV:
                                       self._ctx_ws.data_ptr(), ws)
         self._raw_stream = self.stream.cuda_stream
         self._index, self._lib = self.dev.index, B.lib()
-        # Workspaces of attend, largest last, and how many bytes each size of call needs.  None is let
-        # go of: a captured graph may hold it.
+        # Workspaces of attend, the one in use last: those before it are held by captured graphs.  And how
+        # many bytes each size of call needs.
         self._spaces, self._needs = [], {}
-        self._space_at, self._space_bytes = None, 0
+        self._space_at, self._space_bytes, self._space_held = None, 0, True
 
     # --------------------------------------------------------------------------------------------
     # Checks and descriptors.  A decode step makes these calls once a layer, so they take the tensors'
@@ -267,10 +269,18 @@ class PagedKV:
             need = B.verkv_paged_workspace_size(self.shape, seqs, groups, tokens)
             if need == 0:
                 raise B.VerkvError(B.VERKV_EINVAL, "too many sequences, prefixes or queries")
+            if len(self._needs) >= 4096:
+                self._needs.clear()
             self._needs[key] = need
         if need > self._space_bytes:
-            self._spaces.append(torch.empty(need, dtype=torch.uint8, device=self.dev))
-            self._space_at, self._space_bytes = self._spaces[-1].data_ptr(), need
+            if not self._space_held:
+                self._spaces.pop()
+            # by half at least: calls that grow one by one make few of them
+            size = max(need, self._space_bytes + self._space_bytes // 2)
+            self._spaces.append(torch.empty(size, dtype=torch.uint8, device=self.dev))
+            self._space_at, self._space_bytes, self._space_held = self._spaces[-1].data_ptr(), size, False
+        if not self._space_held and _capturing():
+            self._space_held = True
         return self._space_at, self._space_bytes
 
     def sync(self):
