@@ -69,7 +69,7 @@ def test_workspace_holds_what_any_smaller_call_lays_out():
     size = _workspace_size()
     rng = np.random.default_rng(11)
     log = lambda lo, hi: int(np.exp(rng.uniform(np.log(lo), np.log(hi + 1))))  # noqa: E731
-    for _ in range(20_000):
+    for _ in range(3000):
         h, G, d = int(rng.choice([1, 2, 8])), int(rng.choice([1, 2, 4, 8])), int(rng.choice([64, 128]))
         seqs, groups, q = log(1, 3000), int(rng.integers(0, 2)) * log(1, 3000), log(1, 40000)
         have = size(h, G, d, seqs, groups, q)
@@ -88,3 +88,71 @@ def test_workspace_of_a_prompt_is_in_proportion():
         assert size(8, 4, 128, seqs, 0, q) <= rows * 130 * 4 * 1.2 + (24 << 20)
     # a decode step of 256 sequences behind a prefix
     assert size(8, 4, 128, 256, 1, 256) < 80 << 20
+
+
+# ------------------------------------------------------------------------------------------------
+# Steps of a prompt's row tiles in closed form, and the place of a token's sequence by 32 probes a turn.
+def _ramp(b, n, tt_shift, tile_shift):
+    """csrc/paged.cuh, in its 32-bit arithmetic."""
+    none = 0 if b >= 0 else min(n, -b >> tt_shift)
+    n -= none
+    y = b + ((none + 1) << tt_shift) + (1 << tile_shift) - 1
+    w = n * (y >> tile_shift)
+    u = 0xFFFFFFFF
+    if tt_shift >= tile_shift:
+        return w + (((((n * (n - 1)) & u) >> 1) << (tt_shift - tile_shift)) & u)
+    shift = tile_shift - tt_shift
+    j = n + ((y & ((1 << tile_shift) - 1)) >> tt_shift)
+    q = j >> shift
+    return w + ((((((q * (q - 1)) & u) >> 1) << shift) + (j & ((1 << shift) - 1)) * q) & u)
+
+
+def test_steps_of_row_tiles_in_closed_form():
+    rng = np.random.default_rng(5)
+    for _ in range(2000):
+        tt_shift, tile_shift = int(rng.integers(0, 9)), int(rng.choice([6, 7]))
+        qn, length = int(rng.integers(1, 3000)), int(rng.choice([0, 1, 63, 64, 65, rng.integers(0, 6000)]))
+        tt, T = 1 << tt_shift, 1 << tile_shift
+        nt = -(-qn // tt)
+        # what the last query of a tile sees
+        seen = [min(max(length - (qn - 1 - (min(qn, (k + 1) * tt) - 1)), 0), length) for k in range(nt)]
+        before = np.concatenate([[0], np.cumsum([-(-v // T) for v in seen])])
+        for m in {0, 1, nt // 2, nt - 1, nt} | {int(x) for x in rng.integers(0, nt + 1, 3)}:
+            if m > nt:
+                continue
+            w = -(-length // T) if m == nt and m > 0 else 0
+            if nt > 1:
+                w += _ramp(length - qn, min(m, nt - 1), tt_shift, tile_shift)
+            assert w == before[m], (qn, length, tt, T, m)
+
+
+def test_steps_of_row_tiles_up_to_31_bits():
+    for tt_shift, tile_shift, n, b in ((8, 7, 46000, 0), (5, 7, 130000, -70), (0, 6, 360000, 9), (7, 7, 65000, -129), (8, 6, 32000, 5)):
+        want = sum(-(-max(0, b + ((k + 1) << tt_shift)) // (1 << tile_shift)) for k in range(n))
+        assert want < 1 << 31 and _ramp(b, n, tt_shift, tile_shift) == want
+
+
+def _last_at_most(start, x):
+    at, left, turns = -1, len(start), 0
+    while left > 0:
+        step, turns = (left + 31) >> 5, turns + 1
+        lanes = np.arange(0, min(32 * step, left), step)
+        c = int((start[at + 1 + lanes] <= x).sum())
+        if c == 0:
+            break
+        at += 1 + (c - 1) * step
+        left = min(step, left - (c - 1) * step) - 1
+    return at, turns
+
+
+def test_last_start_at_most():
+    rng = np.random.default_rng(6)
+    for _ in range(1500):
+        n = int(rng.choice([0, 1, 30, 31, 32, 33, 255, 256, 1000, 65536, rng.integers(0, 3000)]))
+        start = np.sort(rng.integers(0, max(2, n), n + 1))
+        start[0] = 0
+        x = int(rng.integers(0, max(2, n)))
+        at, turns = _last_at_most(start, x)
+        assert at == np.searchsorted(start, x, side="right") - 1 and turns <= 4
+        rng.shuffle(start)  # out of order: still an index of the range
+        assert -1 <= _last_at_most(start, x)[0] <= n

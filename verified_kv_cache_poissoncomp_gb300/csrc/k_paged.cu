@@ -444,14 +444,20 @@ __global__ void __launch_bounds__(PG_NT, PG_CTAS)
 }
 
 // ---------------------------------------------------------------------------------------------
-// The last index i of 0 .. n with start[i] <= x (start ascending; -1: none).  The whole warp.
+// The last index i of 0 .. n with start[i] <= x (start ascending; -1: none).  The whole warp: 32 probes a
+// turn, so that 65536 sequences take four.  (Starts out of order end at some index of the range.)
 __device__ __forceinline__ int last_at_most(const int32_t *start, int n, int x) {
-    int c = 0;
-#pragma unroll 4
-    for (int i = threadIdx.x & 31; i <= n; i += 32) c += start[i] <= x ? 1 : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
-    return c - 1;
+    const int lane = threadIdx.x & 31;
+    int at = -1, left = n + 1;  // start[at] <= x; how many behind it are left to look at
+#pragma unroll 1
+    while (left > 0) {
+        const int step = (left + 31) >> 5;
+        const int c = __popc(__ballot_sync(0xFFFFFFFFu, lane * step < left && start[at + 1 + lane * step] <= x));
+        if (c == 0) break;
+        at += 1 + (c - 1) * step;
+        left = min(step, left - (c - 1) * step) - 1;
+    }
+    return at;
 }
 
 constexpr int PM_NT = 128;
