@@ -348,10 +348,10 @@ typedef struct {
     const uint64_t *turns;
 } verkv_rope;
 
-/* turns[j] = frac(inv_freq[j] / (2 pi)) * 2^64, rounded (host arrays of `count` values): the part
- * of a turn that one position makes, in 64-bit fixed point, so that p * turns[j] mod 2^64 is the
- * angle of any 32-bit position to within p * 2^-53 of a turn and its reduction to one turn is
- * exact.  inv_freq must be finite and of magnitude below 2^32 (VERKV_EINVAL). */
+/* turns[j] = frac(inv_freq[j] / (2 pi)) * 2^64 mod 2^64, cut to a whole number (host arrays of `count`
+ * values): the part of a turn that one position makes, in 64-bit fixed point.  p * turns[j] mod 2^64 is the angle of
+ * any 32-bit position p to within p (|inv_freq[j]| 2^-54 + 2^-63) of a turn, and its reduction to one turn
+ * is exact.  inv_freq must be finite and of magnitude below 2^32 (VERKV_EINVAL). */
 verkv_status verkv_rope_turns(const double *inv_freq, int32_t count, uint64_t *turns);
 
 /* Per-head root-mean-square norm x * w / sqrt(mean(x^2) + eps), before the rotation.  q_weight and

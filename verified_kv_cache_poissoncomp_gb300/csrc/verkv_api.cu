@@ -1094,10 +1094,9 @@ verkv_status verkv_rope_turns(const double *inv_freq, int32_t count, uint64_t *t
     for (int32_t i = 0; i < count; ++i)
         if (!isfinite(inv_freq[i]) || fabs(inv_freq[i]) >= 4294967296.0) return VERKV_EINVAL;
     for (int32_t i = 0; i < count; ++i) {
-        const double t = inv_freq[i] / 6.283185307179586476925286766559;
-        const double f = t - floor(t);  // [0, 1]: 1 when t is a hair below a whole number
-        const double x = ldexp(f, 64);
-        turns[i] = x >= 18446744073709551616.0 ? 0u : (uint64_t)x;
+        const double t = fabs(inv_freq[i]) / 6.283185307179586476925286766559;
+        const uint64_t x = (uint64_t)ldexp(t - floor(t), 64);  // (the difference is exact)
+        turns[i] = inv_freq[i] < 0.0 ? 0u - x : x;             // (of a small negative t it would not be)
     }
     return VERKV_OK;
 }
