@@ -224,6 +224,8 @@ class PagedKV:
         rq = self._rows(q, tokens, hq, "q")
         own = prefix = ps = pg = po = pl = None
         groups = 0
+        if (table is None) != (lengths is None) or (prefix_table is None) != (prefix_lengths is None):
+            raise ValueError("a table and its lengths come together")
         if table is not None:
             at, n, stride = self._table(table, "table")
             if n:
