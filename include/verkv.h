@@ -456,7 +456,7 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
  * result as exact as these are.
  * What pages hold behind a length is never used, but a value that is not finite inside it reaches
  * every query of its sequence (or, in a prefix, of its group), also one whose own place comes
- * before it.
+ * before it, and an infinity may come out as not a number.
  * A page id outside the pool, a length outside 0 .. max_length, or q_start or group_start not
  * ascending within their range is latched (verkv_sync returns VERKV_EINVAL); nothing outside the
  * tensors is read or written, and the outputs of that call are not valid. */

@@ -15,14 +15,14 @@
 // two 16-bit parts, its rounding and what that leaves out, so that o is off by its own rounding only (one
 // part: 1.33 times that, behind 32K tokens in bf16).  That doubles the products of P V, or, where no unit
 // has more than 8 rows (a decode step's own tokens), the second parts take the rows that are free.  (256
-// sequences behind 32K tokens: one part 143 us, products of their own 154, free rows 145.)  At a unit's
+// sequences behind 32K tokens: products of their own 156 us, free rows 148.)  At a unit's
 // end the four warps' states are joined in the step's own shared memory, which nothing reads any more,
 // and written as one partial.
 //
 // Measured (d 128, 8 heads, bf16): 32 sequences of up to 16384 tokens (1.1 GB) 168 us a call, 0.97 of a
-// plain copy's bandwidth; 4 behind 128K tokens 93 us, 0.87; 256 sequences of up to 256 tokens 44 us
+// plain copy's bandwidth; 4 behind 128K tokens 94 us, 0.85; 256 sequences of up to 256 tokens 44 us
 // (41 without any arithmetic: their copies, of whole steps, and the start bound it); 8 of up to 512
-// tokens 10.5 us, two launches.
+// tokens 10.8 us, two launches.  At d 128 ptxas spills 4 to 16 bytes a thread of its 168 registers.
 //
 // k_paged_merge: a warp, or with few rows four, per query token and head joins the partials of its
 // prefix and its own pages, and the caller's prior state, in a fixed order.
@@ -646,7 +646,7 @@ cudaError_t launch_paged(const PagedArgs &a, const PagedLine &l, const CUtensorM
 
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedLines &lines, int dtype, int d, cudaStream_t s) {
     const long long rows = (long long)a.q_tokens * (a.hkv << a.g_shift);
-    // Few rows with many partials each (128 rows with 39 each, 128K tokens: 100 -> 93 us a call) have warps to spare.
+    // Few rows with many partials each (128 rows with 39 each, 128K tokens: 101.6 -> 94.3 us a call) have warps to spare.
     double partials = 0.0;  // of a row, about
     for (const PagedLine &l : lines.l)
         if (l.units > 0) partials = std::max(partials, (double)l.ctas / l.units);

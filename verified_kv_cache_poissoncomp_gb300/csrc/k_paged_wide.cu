@@ -28,17 +28,18 @@
 //
 // Weights in two parts leave o off by its own rounding alone (32K tokens, bf16: 1.64e-3 of its root mean
 // square) at twice the products of P V.  With 128 rows the bytes bound a step and that costs little (8
-// sequences behind 32K tokens 40.5 -> 43.9 us).  With 256 rows the products bound it: 256 sequences behind
-// 32K tokens would go from 143 to 217 us, a prompt of 32768 from 11.7 to 14.0 ms.  There the weights are
+// sequences behind 32K tokens 40.9 -> 43.9 us).  With 256 rows the products bound it: 256 sequences behind
+// 32K tokens would go from 148 to 214 us, a prompt of 32768 from 9.0 to 11.4 ms.  There the weights are
 // rounded once, as o is (2.2e-3 in all); the sum they are divided by is not.
 //
 // Measured (8 heads, d 128, bf16; whole calls): 1024 rows a head behind 128K tokens 405 us,
 // 1.36 PFLOP/s, 0.71 of a library matrix product's rate; behind 32K tokens 120 us; 32 rows behind 128K
-// 91 us, 0.87 of a plain copy's bandwidth.  A step of 256 rows takes about 3300 cycles.  Its products
+// 93 us, 0.85 of a plain copy's bandwidth.  A step of 256 rows takes about 3300 cycles.  Its products
 // need 2050 at the tensor core's rate and some 2500 with their operands' reads from shared memory
 // (Q K^T: 82 cycles for 64), and it is they that bound it: a faster maximum, or P announced in smaller
 // parts, changed nothing or lost (the smaller parts 4 %), and Q K^T in two halves lost 25 %.  With
-// d 64 the products halve and the exponentials do not (32K tokens, 1024 rows: 98 us).
+// d 64 the products halve and the exponentials do not (32K tokens, 1024 rows: 98 to 109 us).  A thread has 168
+// registers (ten warps an SM), a softmax row takes 128 of them, and ptxas spills 84 to 120 bytes.
 #include <float.h>
 #include <math.h>
 

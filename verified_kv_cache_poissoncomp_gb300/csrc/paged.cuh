@@ -10,12 +10,13 @@
 // shared by many CTAs and a CTA takes many short ones.  A run that holds the end of one unit and the
 // start of the next costs a CTA about PAGED_SLACK steps more than one piece of the same length: where
 // units are few, each gets the same whole number of runs (`room` steps of the line, its own or not),
-// if they need not be longer by more than that (8 sequences behind 40000 tokens 48.5 -> 43.6 us, 64
-// behind 32768 73.8 -> 68.3).  Lengths are read on the device, so a captured graph follows them.
+// if they need not be longer by more than that (8 sequences behind 40000 tokens 56.3 -> 48.2 us, 64
+// behind 32768 72.5 -> 62.5).  Lengths are read on the device, so a captured graph follows them.
 //
-// The piece of unit u in run c goes to the partial slot c + u: walking the line, each step to the next piece raises exactly one of the two.  Row tiles
-// come before heads so that the CTAs which read the same K and V for other rows do so at about the
-// same time, from the L2 cache (heads first, 1024 rows read a 134 MB prefix four times from memory).
+// The piece of unit u in run c goes to the partial slot c + u: walking the line, each step to the next
+// piece raises exactly one of the two.  Row tiles come before heads so that the CTAs which read the same
+// K and V for other rows do so at about the same time, from the L2 cache (heads first, 1024 rows read a
+// 134 MB prefix four times from memory).
 #pragma once
 
 #include <cuda.h>

@@ -433,9 +433,9 @@ constexpr int PAGED_MAX_SEGMENTS = 65536;  // sequences or prefixes of a call
 int64_t paged_rows(int64_t q_tokens, int64_t segments, int G) { return (q_tokens + segments - 1) / segments * G; }
 
 // Which kernel a level goes through, by the rows of its segments.  Prefixes of up to 16 rows and own
-// tokens of up to 32: k_paged; more: k_paged_wide.  (32 rows of a 32K prefix: k_paged 52 us, reading at
-// 4.5 TB/s for its arithmetic, k_paged_wide 40; own tokens of 32 sequences of 18 rows, up to 4096 each:
-// k_paged 58, k_paged_wide, whose 128 rows are then mostly empty, 77.)
+// tokens of up to 32: k_paged; more: k_paged_wide.  (8 sequences behind 32K tokens, 32 rows:
+// k_paged 55 us, k_paged_wide beside it 44; own tokens of 32 sequences of 18 rows, up to 4096 each:
+// k_paged 65, k_paged_wide, whose 128 rows are then mostly empty, 84.)
 bool paged_wide_prefix(int64_t rows) { return rows > PAGED_ROWS / 2; }
 bool paged_wide_own(int64_t rows) { return rows > PAGED_ROWS; }
 
@@ -504,10 +504,11 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
 // The SMs of a call that launches both kernels.  Their CTAs do not fit on one SM together, and one
 // after the other each leaves the GPU idle while it starts and ends, and the one bound by bytes the
 // tensor cores of the other.  So k_paged gets SMs of its own beside the others, in proportion to the
-// work (8 sequences behind 32K tokens: 43 us one after the other, 40 side by side; 256: 158, 143; 128
-// with up to 1000 tokens of their own: 119, 98), unless it would take most of them.  Costs are the us
+// work (8 sequences behind 32K tokens: 46 us one after the other, 44 side by side; 256: 159, 148; 128
+// with up to 1000 tokens of their own: 120, 98), unless it would take most of them.  Costs are the us
 // of a step on an SM: 0.4 of k_paged, two CTAs an SM, and 0.7 a unit, with 32 rows 1.8 times that; 1.5
-// or 2 of k_paged_wide with 128 or 256 rows.
+// or 2 of k_paged_wide with 128 or 256 rows.  (Measured at d 128; of k_paged 0.45 and 0.5 a step, or 2 times
+// with 32 rows, change nothing by more than the spread between runs.)
 bool paged_share(PagedLine &wide, PagedLine &own, int sms) {
     const double w = wide.cost, o = own.cost;
     int x = (int)(sms * o / (w + o)) + 1;
