@@ -1,10 +1,13 @@
 """What the device arrays of a call hold out of range is reported also where no page is read for it: starts of
 queries that only prefixes are attended for, and lengths of a level whose bound is 0."""
+import math
+
 import pytest
 import torch
 
 from tests.test_gpu_paged import Case, ints
 from verified_kv_cache_poissoncomp_gb300 import binding as B
+from verified_kv_cache_poissoncomp_gb300.paged import PagedKV
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +57,16 @@ def test_many_starts_and_lengths():
     assert status(c, table, lengths, 0, q_start=starts) == B.VERKV_EINVAL
     starts[n - 1], lengths[n - 1] = 2, 0
     assert status(c, table, lengths, 0, q_start=starts) == B.VERKV_EINVAL
+
+
+def test_a_grid_of_more_threads_than_32_bits_count():
+    # 2^21 queries of 64 heads that see nothing: 2^25 blocks of 128 threads, all of which share the checks
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 60 GB")
+    n, h = 1 << 21, 64
+    c = PagedKV(h, 1, 64, num_pages=1)
+    q = torch.zeros((1, h, 64), dtype=torch.bfloat16, device="cuda").expand(n, -1, -1)
+    for starts, want in (([0, n], B.VERKV_OK), ([0, n - 1], B.VERKV_EINVAL), ([1, n], B.VERKV_EINVAL)):
+        o, lse = c.attend(0, q, None, None, 0, q_start=ints(starts))
+        assert B.verkv_sync_status(c.ctx) == want
+    assert not o[::4096].any() and bool((lse == -math.inf).all())

@@ -462,9 +462,10 @@ __device__ __forceinline__ int last_at_most(const int32_t *start, int n, int x) 
 
 constexpr int PM_NT = 128;
 
-// start[0 .. n] ascends from 0 to `end`, or the call is reported; all threads of the grid.
+// start[0 .. n] ascends from 0 to `end`, or the call is reported; all threads of the grid, whose number may
+// pass 32 bits.
 __device__ __forceinline__ void check_starts(const PagedArgs &a, const int32_t *start, int n, int end) {
-    for (int i = blockIdx.x * PM_NT + threadIdx.x; i <= n; i += gridDim.x * PM_NT) {
+    for (long long i = (long long)blockIdx.x * PM_NT + threadIdx.x; i <= n; i += (long long)gridDim.x * PM_NT) {
         const int x = start[i];
         if (i == n ? x != end : x > start[i + 1] || (i == 0 && x != 0)) raise_error(a.err, ERR_PAGE);
     }
@@ -474,7 +475,7 @@ static __device__ __noinline__ void check_unseen(const PagedArgs &a) {
     if (a.check_q_start) check_starts(a, a.q_start, a.seqs, a.q_tokens);
     if (a.check_group_start) check_starts(a, a.group_start, a.zero_rows[0], a.seqs);
     for (int x = 0; x < 2; ++x)
-        for (int i = blockIdx.x * PM_NT + threadIdx.x; i < a.zero_rows[x]; i += gridDim.x * PM_NT)
+        for (long long i = (long long)blockIdx.x * PM_NT + threadIdx.x; i < a.zero_rows[x]; i += (long long)gridDim.x * PM_NT)
             if (a.zero_length[x][i] != 0) raise_error(a.err, ERR_PAGE);
 }
 

@@ -40,7 +40,8 @@ class PagedKV:
     """A pool of pages [layers][num_pages][kv_heads][page_tokens][2][head_dim] and the calls on it.
     Work is issued on the stream that is current when the object is made; a call made while another
     is current is refused.  One object's calls share its workspace: graphs that may run at the same
-    time need an object each (kv= adopts an existing pool).  With num_pages=0 it has no pool and only
+    time need an object each (kv= adopts an existing pool), and a graph needs its object as long as it
+    is replayed.  With num_pages=0 it has no pool and only
     norm_rotate."""
 
     def __init__(self, kv_heads, q_per_kv, head_dim, page_tokens=64, num_pages=0, layers=1,
