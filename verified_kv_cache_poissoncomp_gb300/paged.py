@@ -41,8 +41,7 @@ class PagedKV:
     Work is issued on the stream that is current when the object is made; a call made while another
     is current is refused.  One object's calls share its workspace: graphs that may run at the same
     time need an object each (kv= adopts an existing pool), and a graph needs its object as long as it
-    is replayed.  With num_pages=0 it has no pool and only
-    norm_rotate."""
+    is replayed.  With num_pages=0 it has no pool and only norm_rotate."""
 
     def __init__(self, kv_heads, q_per_kv, head_dim, page_tokens=64, num_pages=0, layers=1,
                  dtype=torch.bfloat16, device=None, kv=None):
