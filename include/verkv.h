@@ -458,9 +458,11 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
  *   workspace device, 256-byte aligned, at least verkv_paged_workspace_size bytes; calls that may
  *             run at the same time (graphs replayed on other streams among them) need one each
  * Logits, the running maximum and sum, and the partial sums are float32.  Over 4-bit pages K and V enter
- * as exactly what they stand for, and a weight is rounded to binary16, once where it meets floors and twice where it
- * meets codes (2^-11 in all), and not in the sum they are divided by; with binary16 rows what that leaves
- * out goes along (2^-22).  Units
+ * as exactly what they stand for, and a weight is rounded to binary16, once where it meets floors (2^-11) and twice where
+ * it meets codes (2^-10 in all), and not in the sum they are divided by; with binary16 rows what that leaves
+ * out goes along (2^-22, and of codes 2^-20).  Of weights far below a row's largest a token loses up to 2^-32 of
+ * that, of its floors, and 15 2^-30 of it, of the largest step of its group of channels (of 2^-16 where
+ * all of a group's steps are smaller); and where steps of 1 and more come, smaller ones are off by 2^-24 of them.  Units
  * have at most 16 rows there, so many queries of one sequence or prefix read its codes again for every 16
  * (from 128 rows on, 16-bit pages are the faster ones).  Over 16-bit pages the weights are multiplied
  * with V as two parts of the pages' type, which hold them to 2^-16 (bf16) or 2^-22 (fp16); where

@@ -11,17 +11,21 @@
 //     S = K Q^T      16 tokens x 8 rows, exact codes (q4.cuh), steps and floors after it in float32
 //     P = 2^(S c - ref), rounded to binary16 and turned into a B operand by a transpose of 8 x 8 tiles
 //         (movmatrix); times the step of each group of V's channels, rounded again: an operand a group.  Of
-//         bfloat16 results that is all: a weight is off by 2^-12, and 2^-12 more where it meets codes, little
-//         beside the result's own 2^-9 (1.66e-3 of o's root mean square, 1.65e-3 without).  Binary16 results
+//         bfloat16 results that is all: a weight is off by up to 2^-11, and 2^-11 more where it meets codes, little
+//         beside the result's own 2^-8 (1.66e-3 of o's root mean square, 1.65e-3 without).  Binary16 results
 //         would show it (5.5e-4 for 2.1e-4): there what either rounding leaves out goes along in an operand of
 //         its own (REST).  The sum that they are divided by is of the float32 weights
 //     O += V^T P     channels x rows, exact codes
 //     B += F^T P     groups x rows: the floors' part, the same for all channels of a group
 //
 // `ref` of a row is its running maximum at some step, and is raised, with O scaled, only where the
-// maximum has risen by more than SLACK since: a vote a block, and shuffles in the rare other case.  It keeps P
-// below 2^13, and where steps of 2 and more come it takes on their power of two, so that P times a step is
-// below 2^14: within binary16, with 38 bits of it below the largest.
+// maximum has risen by more than SLACK since: a vote a block, and shuffles in the rare other case.  P is below
+// 2^14, the largest one so far 2^8 at least, and the last bit of a binary16 2^-24.  Steps meet it as step 2^k, with a k for each
+// group of V's channels that makes the largest one so far 1/2 to 2 (k <= 15, all that one product makes of binary16:
+// a group whose steps are all below 2^-16 stays below 1/2).  Where larger steps come k is lowered, with O scaled, by
+// the same vote.  So products are below 2^15, and as many bits of them remain in small values as in
+// large ones: a token loses 2^-33 of the row's largest weight times its group's largest step.  (With steps as
+// they are, codes of values of 0.01 behind a token of 2^20 times the others' weight were off by a quarter.)
 //
 // Bound: with few rows the bytes, and the start, end and merge of a CTA's run (11-17 us): 32 sequences of up to
 // 16384 tokens (346 MB) 80 us, 0.64 of a plain copy's rate over all and 6.0 TB/s, 0.88, in the steady part (the same
@@ -43,7 +47,9 @@ namespace {
 
 constexpr int PQ_WARPS = 4, PQ_NT = 32 * PQ_WARPS;
 constexpr int PQ_NS = 4;  // blocks of a warp's ring
+constexpr float PQ_ROOM = 14.0f;  // log2 that a weight may be above ref
 constexpr float PQ_SLACK = 6.0f;  // log2 that a maximum may rise by until ref does
+constexpr uint32_t PQ_SCALE = 0x78007800u;  // 2^15, twice: of a group before its first steps
 constexpr float PQ_NONE = -1e30f;                // ref of a row that has seen nothing
 
 struct Q4Piece {
@@ -237,8 +243,9 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[n][x][e] = 0.0f;
         }
-        uint32_t most = 15;  // exponent bits of the largest step so far, from 2 on: steps are below 2^(most - 14)
-        float room = 13.0f;  // what a logit may be above ref: 28 - most
+        uint32_t scale[NG];  // of a group's steps, 2^k twice: o is 2^k times what it stands for
+#pragma unroll
+        for (int x = 0; x < NG; ++x) scale[x] = PQ_SCALE;
 
         int b = 0;
 #pragma unroll 1
@@ -249,14 +256,25 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
             const int tok = tok0 + b * PAGED_TILE;
             // V's floors and steps of tokens 2 t and 2 t + 1, and of 8 more: pairs of tokens, [8 more][group]
             uint32_t steps2[2][NG], floors2[2];
+            auto load_steps = [&]() {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const unsigned char *par = st + F::SIDE + F::PARS + (2 * t + 8 * i) * F::PAR;
+                    const KeyVec x = *reinterpret_cast<const KeyVec *>(par), y = *reinterpret_cast<const KeyVec *>(par + F::PAR);
+#pragma unroll
+                    for (int z = 0; z < NG; ++z) steps2[i][z] = byte_pair(word_of(x, z), word_of(y, z), 0x7632u);
+                }
+            };
+            // what lies behind the tokens that are seen may be anything, not a number too
+            auto seen = [&](int i) -> uint32_t {
+                const int left = vis - (tok + 2 * t + 8 * i);
+                return left <= 0 ? 0u : left == 1 ? 0xFFFFu : 0xFFFFFFFFu;
+            };
+            load_steps();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const unsigned char *par = st + F::SIDE + F::PARS + (2 * t + 8 * i) * F::PAR;
-                const KeyVec x = *reinterpret_cast<const KeyVec *>(par), y = *reinterpret_cast<const KeyVec *>(par + F::PAR);
-#pragma unroll
-                for (int z = 0; z < NG; ++z) steps2[i][z] = byte_pair(word_of(x, z), word_of(y, z), 0x7632u);
-                const int own = (g & (NG - 1)) * 4;
-                floors2[i] = byte_pair(*reinterpret_cast<const uint32_t *>(par + own), *reinterpret_cast<const uint32_t *>(par + F::PAR + own), 0x5410u);
+                const unsigned char *par = st + F::SIDE + F::PARS + (2 * t + 8 * i) * F::PAR + (g & (NG - 1)) * 4;
+                floors2[i] = byte_pair(*reinterpret_cast<const uint32_t *>(par), *reinterpret_cast<const uint32_t *>(par + F::PAR), 0x5410u);
             }
             float s[NT][4], y[NT][4];
             {
@@ -275,27 +293,22 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[n][e] = tok + g + 8 * (e >> 1) < lim[n][e & 1] ? s[n][e] : -INFINITY;
-                // what lies behind the tokens that are seen may be anything, not a number too
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int left = vis - (tok + 2 * t + 8 * i);
-                    const uint32_t seen = left <= 0 ? 0u : left == 1 ? 0xFFFFu : 0xFFFFFFFFu;
-                    floors2[i] &= seen;
+                    floors2[i] &= seen(i);
 #pragma unroll
-                    for (int z = 0; z < NG; ++z) steps2[i][z] &= seen;
+                    for (int z = 0; z < NG; ++z) steps2[i][z] &= seen(i);
                 }
             }
-            // Does any step reach 2?  Its bit 14 says so; the largest one is looked for only then.
+            // Does any step reach 2?  Its bit 14 says so (of one that has become infinite too); the largest ones are looked
+            // for only then.
             uint32_t step = 0;
 #pragma unroll
-            for (int z = 0; z < 2 * NG; ++z) step |= steps2[z / NG][z % NG];
-            step &= 0x40004000u;
-            if (step) {
-                step = 0;
-#pragma unroll
-                for (int z = 0; z < 2 * NG; ++z) step = max_f16(step, steps2[z / NG][z % NG]);
-                step = max(step & 0xFFFFu, step >> 16) >> 10;
+            for (int z = 0; z < 2 * NG; ++z) {
+                steps2[z / NG][z % NG] = mul_f16(steps2[z / NG][z % NG], scale[z % NG]);
+                step |= steps2[z / NG][z % NG];
             }
+            step &= 0x40004000u;
             float above = -INFINITY;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -304,10 +317,35 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                     y[n][e] = fmaf(s[n][e], unit[n][e & 1], -ref[n][e & 1]);
                     above = fmaxf(above, y[n][e]);
                 }
-            if (__any_sync(0xFFFFFFFFu, above > room || step > most)) {
-                const uint32_t was = most;
-                most = max(most, __reduce_max_sync(0xFFFFFFFFu, step));
-                room -= (float)(most - was);
+            if (__any_sync(0xFFFFFFFFu, above > PQ_ROOM || step)) {
+                if (__any_sync(0xFFFFFFFFu, step)) {
+                    load_steps();
+#pragma unroll
+                    for (int z = 0; z < NG; ++z) {
+                        if (tok + 16 > lim0) {
+                            steps2[0][z] &= seen(0);
+                            steps2[1][z] &= seen(1);
+                        }
+                        uint32_t top = max_f16(steps2[0][z], steps2[1][z]);
+                        top = max(top & 0xFFFFu, top >> 16) >> 10;  // exponent bits
+                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                        // (all lanes hold the same.  2^-15 is the one power below binary16's normal numbers that may be
+                        // needed: its exponent bits are 0, as the k that they stand for has it)
+                        const int was = (int)(scale[z] >> 10 & 31u) - 15, k = (int)top + was >= 16 ? max(14 - (int)top, -15) : was;
+                        scale[z] = k == -15 ? 0x02000200u : (uint32_t)(k + 15) * 0x04000400u;
+                        const float f = __uint_as_float((uint32_t)(127 + k - was) << 23);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                o[n][2 * z][e] *= f;
+                                o[n][2 * z + 1][e] *= f;
+                            }
+                        steps2[0][z] = mul_f16(steps2[0][z], scale[z]);
+                        steps2[1][z] = mul_f16(steps2[1][z], scale[z]);
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float f[2];
@@ -316,7 +354,7 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                         float top = fmaxf(s[n][e], s[n][e + 2]);
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                        const float m = fmaxf(ref[n][e] + (float)(most - was), fmaf(top, unit[n][e], PQ_SLACK - room));
+                        const float m = fmaxf(ref[n][e], fmaf(top, unit[n][e], PQ_SLACK - PQ_ROOM));
                         f[e] = exp2_fast(ref[n][e] - m);  // (nothing summed yet: 0 or 1)
                         ref[n][e] = m;
                         sum[n][e] *= f[e];
@@ -421,6 +459,9 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
         // which holds nothing any more, and all threads add the four and write the partial.
         float *buf = reinterpret_cast<float *>(pq_smem);
         float base[NT][2][NG];  // the floors' part
+        float back[NG];         // 2^-k
+#pragma unroll
+        for (int x = 0; x < NG; ++x) back[x] = __uint_as_float((254u << 23) - __float_as_uint(floor_of(scale[x])));
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -450,7 +491,7 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                     // channels 16 x + 2 g and the next one, or of d = 64 16 x + g and 8 more; codes of upper bits are 16 n
                     float *at = buf + (warp * R + r) * D + 16 * x;
                     const float lu = D == 128 && (x & 1) ? CODE_UNIT / 16 : CODE_UNIT, hu = D == 64 || (x & 1) ? CODE_UNIT / 16 : CODE_UNIT;
-                    const float lo = fmaf(o[n][x][e], lu, base[n][e][x / 2]) * f, hi = fmaf(o[n][x][e + 2], hu, base[n][e][x / 2]) * f;
+                    const float lo = fmaf(o[n][x][e], lu * back[x / 2], base[n][e][x / 2]) * f, hi = fmaf(o[n][x][e + 2], hu * back[x / 2], base[n][e][x / 2]) * f;
                     if (D == 128) {
                         *reinterpret_cast<float2 *>(at + 2 * g) = make_float2(lo, hi);
                     } else {
