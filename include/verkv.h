@@ -164,7 +164,9 @@ verkv_status verkv_create(verkv_ctx **ctx, int device, void *stream, const verkv
                           void *workspace, size_t workspace_bytes);
 
 /* Release the side stream, events, staging and thread pool (after synchronising).  May be called while a
- * graph is being captured, on this stream or another. */
+ * graph is being captured, on this stream or another.  While the context's own stream is captured it waits for the
+ * work on its own host buffers alone: the caller's memory (workspace, host_kv, outputs) that calls made before the capture
+ * use must then be kept until they are done. */
 void verkv_destroy(verkv_ctx *ctx);
 
 /* Select VERKV_FETCH_ZEROCOPY or VERKV_FETCH_MEMCPY, optionally or-ed with VERKV_FETCH_KEYS.

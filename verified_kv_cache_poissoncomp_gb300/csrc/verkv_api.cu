@@ -183,7 +183,9 @@ struct verkv_ctx {
     int device = 0;
     int sms = 0;
     cudaStream_t main = nullptr, side = nullptr;
-    cudaEvent_t e_sel = nullptr, e_fetch = nullptr;
+    // Of MEMCPY mode.  e_sel: behind the last selection made outside a capture, the last to touch the host buffers on
+    // `main`; e_cap: behind one in a capture; selected: which of the two the last selection has.
+    cudaEvent_t e_sel = nullptr, e_fetch = nullptr, e_cap = nullptr, selected = nullptr;
     verkv_shape sh{};
     Layout L{};
     unsigned char *ws = nullptr;
@@ -641,13 +643,16 @@ verkv_status verkv_create(verkv_ctx **out, int device, void *stream, const verkv
 void verkv_destroy(verkv_ctx *ctx) {
     if (!ctx) return;
     // An object may go at any time, also while a graph is being captured (a collector decides): this thread's calls
-    // here do not count against a capture then, and a stream that is capturing itself, which has nothing of the
-    // context's left to wait for, is not waited for.
+    // here do not count against a capture then.  A stream that is capturing itself cannot be waited for, nor one that may
+    // not be asked (the default stream beside a capture), though what was launched before may still run: of that,
+    // only selections touch memory that goes here, and the last one's event can be waited for.
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaThreadExchangeStreamCaptureMode(&mode);
     cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-    if (ctx->main && cudaStreamIsCapturing(ctx->main, &capturing) == cudaSuccess && capturing == cudaStreamCaptureStatusNone)
-        cudaStreamSynchronize(ctx->main);
+    const cudaError_t asked = cudaStreamIsCapturing(ctx->main, &capturing);
+    if (asked != cudaSuccess) cudaGetLastError();
+    if (asked == cudaSuccess && capturing == cudaStreamCaptureStatusNone) cudaStreamSynchronize(ctx->main);
+    else if (ctx->e_sel) cudaEventSynchronize(ctx->e_sel);
     if (ctx->side) cudaStreamSynchronize(ctx->side);
     delete ctx->pool;
     if (ctx->host_staging) cudaFreeHost(ctx->host_staging);
@@ -656,6 +661,7 @@ void verkv_destroy(verkv_ctx *ctx) {
     for (cudaEvent_t e : ctx->prof_pool) cudaEventDestroy(e);
     if (ctx->e_sel) cudaEventDestroy(ctx->e_sel);
     if (ctx->e_fetch) cudaEventDestroy(ctx->e_fetch);
+    if (ctx->e_cap) cudaEventDestroy(ctx->e_cap);
     if (ctx->side) cudaStreamDestroy(ctx->side);
     cudaThreadExchangeStreamCaptureMode(&mode);
     delete ctx;
@@ -677,6 +683,7 @@ verkv_status verkv_set_fetch_mode(verkv_ctx *ctx, int mode_flags) {
     if (mode == VERKV_FETCH_MEMCPY && !ctx->host_staging) {
         const size_t rows = (size_t)ctx->L.units_layer * ctx->sh.n;
         VERKV_CUDA(cudaSetDevice(ctx->device), "cudaSetDevice");
+        if (!ctx->e_cap) VERKV_CUDA(cudaEventCreateWithFlags(&ctx->e_cap, cudaEventDisableTiming), "cudaEventCreate");
         VERKV_CUDA(cudaHostAlloc((void **)&ctx->host_staging,
                                  staging_bytes(ctx->L.units_layer, ctx->sh.n, ctx->sh.head_dim),
                                  cudaHostAllocDefault), "cudaHostAlloc(staging)");
@@ -869,8 +876,12 @@ verkv_status verkv_attend_verified(verkv_ctx *ctx, int32_t layer, const void *q,
                    return launch_certify(ca, ctx->L.qh_layer, certify_smem_bytes(ca.chunk), ctx->main);
                }), "k_certify");
     // MEMCPY mode: verkv_fetch_refine waits on the host for the selection
-    if (ctx->fetch_mode != VERKV_FETCH_ZEROCOPY)
-        VERKV_CUDA(cudaEventRecord(ctx->e_sel, ctx->main), "cudaEventRecord");
+    if (ctx->fetch_mode != VERKV_FETCH_ZEROCOPY) {
+        cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+        VERKV_CUDA(cudaStreamIsCapturing(ctx->main, &capturing), "cudaStreamIsCapturing");
+        ctx->selected = capturing == cudaStreamCaptureStatusNone ? ctx->e_sel : ctx->e_cap;
+        VERKV_CUDA(cudaEventRecord(ctx->selected, ctx->main), "cudaEventRecord");
+    }
 
     // The pivotal partial sums need only the selection: in MEMCPY mode they run here, during the
     // host gather; the zero-copy refine kernel of verkv_fetch_refine does them itself.
@@ -973,7 +984,7 @@ verkv_status verkv_fetch_refine(verkv_ctx *ctx, const int32_t *ids, const int32_
                        return launch_refine(piv, pa, ctx->L.units_layer, grid, ctx->main);
                    }), "k_refine");
     } else {
-        VERKV_CUDA(cudaEventSynchronize(ctx->e_sel), "cudaEventSynchronize");
+        VERKV_CUDA(cudaEventSynchronize(ctx->selected), "cudaEventSynchronize");
         // When profiling, two events on the (idle) side stream bracket the host gather.
         cudaEvent_t g0 = ctx->prof_on ? prof_event(ctx) : nullptr;
         if (g0) VERKV_CUDA(cudaEventRecord(g0, ctx->side), "cudaEventRecord");
