@@ -497,7 +497,8 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
  * and prior), it is the token's share of each query's attention.
  *   seqs, q_tokens, q, q_start, own, scale, and pages of either kind: as in verkv_paged_attend (several
  *             queries are a sequence's last tokens); a sequence may have no query
- *   lse       device float [q_tokens][kv_heads * q_per_kv]; a query whose lse is -infinity adds nothing
+ *   lse       device float [q_tokens][kv_heads * q_per_kv]; a query whose lse is -infinity adds nothing,
+ *             whatever its channels hold (padding)
  *   weights_in  device float [seqs][kv_heads][places], or NULL: zeros
  *   weights_out  the same, and may be weights_in itself (other overlap is not allowed).  Places behind a
  *             length are as in weights_in there

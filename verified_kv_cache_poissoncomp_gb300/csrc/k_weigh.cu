@@ -247,7 +247,9 @@ __device__ __forceinline__ void add_weights(float (&z)[2], const float (&s)[4], 
     }
 }
 
-// lse in units of log 2; a row that saw nothing counts nothing.
+// lse in units of log 2; a row that saw nothing counts nothing.  (Its weights are 2^(s - infinity) = 0 where its channels are
+// numbers.  They need not be, in a padded batch, so it is masked as well: where a tile has such a row, it goes the way
+// of those whose rows do not see every token.)
 __device__ __forceinline__ float lse_log2(float lse) { return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f; }
 
 __device__ __forceinline__ int page_of(const WeighArgs &a, int s, int tok) {
@@ -316,6 +318,7 @@ __global__ void __launch_bounds__(WF_NT, PACKED ? 4 : 2) k_weigh_few(const __gri
         typename K::Queries q;
         float lse2[2], unit[2];
         int lim[2];
+        bool dead = false;  // some of the rows count nothing
         auto take = [&](int r0) {  // rows r0 .. r0 + 7
             const int r = r0 + g, jj = r >> a.g_shift;
             q.load(r < rows ? a.q + (long long)(sq.q0 + jj) * a.q_ts + (long long)((head << a.g_shift) + r - (jj << a.g_shift)) * a.q_hs : nullptr, sign);
@@ -325,7 +328,9 @@ __global__ void __launch_bounds__(WF_NT, PACKED ? 4 : 2) k_weigh_few(const __gri
                 const int y = r0 + 2 * t + e, j = y >> a.g_shift;
                 lim[e] = first + j;
                 lse2[e] = y < rows ? lse_log2(a.lse[((long long)(sq.q0 + j) * a.hkv << a.g_shift) + (head << a.g_shift) + y - (j << a.g_shift)]) : INFINITY;
+                if (lse2[e] == INFINITY) lim[e] = 0;
             }
+            dead = __any_sync(0xFFFFFFFFu, (lim[0] == 0 && r0 + 2 * t < rows) || (lim[1] == 0 && r0 + 2 * t + 1 < rows));
         };
         // Rows in the pool of 32 blocks at a time, one a lane.
         int ids0 = b0, ids = 0;
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(WF_NT, PACKED ? 4 : 2) k_weigh_few(const __gri
                 float lg[NU][4];
 #pragma unroll
                 for (int u = 0; u < NU; ++u) K::logits(lg[u], key[u], ready[u], q);
-                if (b * 16 + 16 * NU <= first + (r0 >> a.g_shift)) {
+                if (b * 16 + 16 * NU <= first + (r0 >> a.g_shift) && !dead) {
 #pragma unroll
                     for (int u = 0; u < NU; ++u) add_weights(z[u], lg[u], unit, lse2);
                 } else {
@@ -522,10 +527,11 @@ __global__ void __launch_bounds__(WM_NT, PACKED ? 3 : 4) k_weigh_many(const __gr
                 for (int e = 0; e < 2; ++e) {
                     unit[e] = K::unit(q, c, e);
                     lse2[e] = lse_at[buf * WM_ROWS + n + 2 * t + e];
-                    // (what is in the place of a row that is not there may be no number)
-                    lim[e] = r0 + n + 2 * t + e < rows ? first + ((r0 + n + 2 * t + e) >> a.g_shift) : 0;
+                    // (what is in the place of a row that is not there may be no number; its lse is infinite)
+                    lim[e] = lse2[e] != INFINITY ? first + ((r0 + n + 2 * t + e) >> a.g_shift) : 0;
                 }
-                const int all = r0 + n + 8 <= rows ? first + ((r0 + n) >> a.g_shift) : 0;  // tokens every one of the rows sees
+                const bool live = __all_sync(0xFFFFFFFFu, lse2[0] != INFINITY && lse2[1] != INFINITY);
+                const int all = live ? first + ((r0 + n) >> a.g_shift) : 0;  // tokens every one of the rows sees
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     float lg[4];
@@ -839,15 +845,16 @@ __global__ void __launch_bounds__(WW_NT, 1)
             unsigned long long sum[4] = {0ull, 0ull, 0ull, 0ull};  // pairs
             for (int t = t0; t < it.tiles; t += 2) {
                 __syncwarp();
+                const bool live = lse[0] != -INFINITY && lse[1] != -INFINITY && lse[2] != -INFINITY && lse[3] != -INFINITY;
                 reinterpret_cast<float4 *>(lse_at)[lane] = make_float4(-lse_log2(lse[0]), -lse_log2(lse[1]), -lse_log2(lse[2]), -lse_log2(lse[3]));
                 __syncwarp();
                 if (t + 2 < it.tiles) fetch(t + 2);
                 const int acc = 2 * m + turn;
                 if (!(go = wait(&s_full[acc], (uint32_t)((tiles + t) / 2)))) break;
                 tcgen05_after_sync();
-                // rows `from` .. `to` - 1 of the tile are there and see this token
-                const int row0 = (it.n0 + t) << 7, from = (max(0, tok - it.first + 1) << a.g_shift) - row0, to = it.rows - row0;
-                const bool all = __all_sync(0xFFFFFFFFu, from <= 0 && to >= 128);
+                // rows from `from` on see this token; those that are not there have an infinite lse
+                const int row0 = (it.n0 + t) << 7, from = (max(0, tok - it.first + 1) << a.g_shift) - row0;
+                const bool all = __all_sync(0xFFFFFFFFu, from <= 0 && live);
 #pragma unroll 1
                 for (int x = 0; x < 128; x += 32) {
                     uint32_t u[32];
@@ -869,8 +876,8 @@ __global__ void __launch_bounds__(WW_NT, 1)
                     } else {
 #pragma unroll
                         for (int y = 0; y < 32; ++y) {
-                            const float e = exp2_fast(fmaf(__uint_as_float(u[y]), c, lse_at[x + y]));
-                            add2(sum[y & 3], x + y < from || x + y >= to ? 0.0f : e, 0.0f);
+                            const float l = lse_at[x + y], e = exp2_fast(fmaf(__uint_as_float(u[y]), c, l));
+                            add2(sum[y & 3], x + y < from || l == -INFINITY ? 0.0f : e, 0.0f);
                         }
                     }
                 }
