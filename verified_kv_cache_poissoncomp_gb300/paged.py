@@ -22,8 +22,13 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 # New CUDA tensors by a call that goes past the dispatcher, whose code a launch has driven out of the host's caches
-# (behind one torch.empty takes 5 to 7 us, this 3), where torch offers that.
+# (behind one torch.empty takes 5 to 7 us, this 3), where torch offers that and nobody has changed what torch.empty does:
+# it passes by dispatch modes, which may count or replace tensors, and by the filling of deterministic algorithms.
 _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+_dispatch_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+_deterministic = getattr(torch._C, "_get_deterministic_algorithms", None)
+if _dispatch_modes is None or _deterministic is None:
+    _empty_strided = None
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 _DTYPES = {torch.bfloat16: B.VERKV_BF16, torch.float16: B.VERKV_F16}
@@ -118,7 +123,7 @@ class PagedKV:
             raise ValueError("another stream is current than the one this object was made on")
 
     def _empty(self, shape, dtype):
-        if _empty_strided is None or min(shape) < 1 or _current_device() != self._index:
+        if _empty_strided is None or _dispatch_modes() or _deterministic() or min(shape) < 1 or _current_device() != self._index:
             return torch.empty(shape, dtype=dtype, device=self.dev)
         if len(shape) == 3:
             return _empty_strided(shape, (shape[1] * shape[2], shape[2], 1), dtype)
