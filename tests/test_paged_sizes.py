@@ -91,4 +91,10 @@ def test_what_is_allowed_goes_on(cache):
     # no lengths, no places: nothing to do
     assert cache.weigh(0, q, lse, table, n, 0).shape == (3, 2, 0)
     assert len(cache._lib.calls) == 4
+    # no sequences: nothing to do, whatever the sizes
+    q, lse, table, n = operands(0)
+    assert cache.weigh(0, q, lse, table, n, 64).shape == (0, 2, 64)
+    assert cache.weigh(0, q, lse, table, n, 64, places(10, 0)).shape == (0, 2, 10)
+    assert cache.evict(0, table, n, 64, places(10, 0), 32, 4, 32)[1].shape == (0, 2, 32)
+    assert len(cache._lib.calls) == 4
     assert isinstance(cache._lib.calls[2][1][3], B.verkv_span) and ctypes.sizeof(B.verkv_span) == 40 - 8

@@ -328,9 +328,9 @@ class PagedKV:
             raise ValueError(f"{name}: a contiguous float32 {list(shape)} tensor on {self.dev} is required")
         return t.data_ptr()
 
-    def _places(self, places, max_length):
-        """Sizes as the library takes them: of 32 bits, and with room for the lengths."""
-        if not 0 <= max_length <= places <= 1 << 30:
+    def _places(self, seqs, places, max_length):
+        """Sizes as the library takes them: of 32 bits, and with room for the lengths (of any sequences)."""
+        if seqs and not 0 <= max_length <= places <= 1 << 30:
             raise ValueError(f"places: as many as max_length ({max_length}) or more, and at most 2^30, are required")
 
     def _apart(self, a, b, shape):
@@ -358,7 +358,7 @@ class PagedKV:
         if lse.dtype is not torch.float32 or lse.device != self.dev or lse.shape != (tokens, hq) or not lse.is_contiguous():
             raise ValueError(f"lse: a contiguous float32 [{tokens}][{hq}] tensor on {self.dev} is required")
         if out is None and weights is None:
-            self._places(max_length, max_length)
+            self._places(n, max_length, max_length)
             out = self._empty((n, self.h, max_length), torch.float32)
         elif out is None:
             out = weights
@@ -366,7 +366,7 @@ class PagedKV:
         if len(shape) != 3:
             raise ValueError("out: a float32 tensor [sequences][kv_heads][places] is required")
         shape = (n, self.h, shape[2])
-        self._places(shape[2], max_length)
+        self._places(n, shape[2], max_length)
         po = self._weights(out, shape, "out")
         pi = None
         if weights is not None:
@@ -398,14 +398,16 @@ class PagedKV:
         if len(shape) != 3:
             raise ValueError("weights: a float32 tensor [sequences][kv_heads][places] is required")
         shape = (n, self.h, shape[2])
-        self._places(shape[2], max_length)
+        self._places(n, shape[2], max_length)
         pi = po = self._weights(weights, shape, "weights")
         if out is None:
             out = weights
         elif out is not weights:
             po = self._apart(pi, self._weights(out, shape, "out"), shape)
-        if not 1 <= keep < 1 << 31 or first < 0 or last < 0 or first + last > keep:
-            raise ValueError("keep: 1 or more, with the first and the last in it")
+        if not 1 <= keep < 1 << 31:
+            raise ValueError("keep: 1 or more")
+        if n and (first < 0 or last < 0 or first + last > keep):
+            raise ValueError("keep: must hold the first and the last")
         if kept is None:
             kept = self._empty((n, self.h, keep), torch.int32)
             pk = kept.data_ptr()
