@@ -462,9 +462,12 @@ int64_t paged_level_rows(int64_t G, int64_t segs, int64_t q_tokens) {
 // Of any call for up to these sizes: both levels, or without prefixes only the sequences' own, and the slots
 // of its launches' CTAs.
 int64_t paged_rows_bound(int64_t hkv, int64_t G, int64_t seqs, int64_t groups, int64_t q_tokens) {
-    // (of k_paged, or over 4-bit pages of a launch of each level)
-    const int64_t rows = q_tokens * G;
-    const int64_t few = std::max<int64_t>(PAGED_MAX_CTAS * PAGED_ROWS, PAGED_Q4_CTAS_32 * 32 * (groups ? 2 : 1));
+    // (of k_paged, or over 4-bit pages of a launch of each level: tiles of 32 rows there are only with more than 16 rows, where
+    // there is room for k_paged_wide's; of fewer rows, paged_q4_share keeps within k_paged's)
+    const int64_t rows = q_tokens * G, few = PAGED_MAX_CTAS * PAGED_ROWS;
+    static_assert(PAGED_Q4_CTAS_32 * 32 <= PAGED_MAX_CTAS * PAGED_ROWS && PAGED_Q4_CTAS_16 * 16 <= PAGED_MAX_CTAS * PAGED_ROWS &&
+                      PAGED_Q4_CTAS * 8 * 2 <= PAGED_MAX_CTAS * PAGED_ROWS && PAGED_Q4_CTAS_32 * 32 <= PAGED_WIDE_CTAS * 128,
+                  "slots of k_paged_q4");
     const int64_t wide = (int64_t)PAGED_WIDE_CTAS * (rows > 128 ? 256 : rows > PAGED_ROWS / 2 ? 128 : 0);
     if (groups == 0) return hkv * paged_level_rows(G, seqs, q_tokens) + std::max(few, wide);
     return hkv * (paged_level_rows(G, seqs, q_tokens) + paged_level_rows(G, groups, q_tokens)) + few + wide;
@@ -479,13 +482,11 @@ size_t paged_workspace(const verkv_shape &sh, int64_t seqs, int64_t groups, int6
     return 256 + rec + rows * (size_t)(sh.head_dim + 2) * 4 + PAGED_LINES * 512;
 }
 
-// Fills in a line over the given segments, taking its buffers from the workspace at `off`; false if
-// its work cannot be counted in 31 bits.
-bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows_tile, int ctas_max, unsigned char *ws,
-                size_t &off) {
+// Fills in a line over the given segments but its buffers; false if its work cannot be counted in 31 bits.
+bool paged_count(const PagedArgs &a, PagedLine &l, int rows_tile, int ctas_max) {
     const int64_t hkv = a.hkv;
     l.tt_shift = log2_of(rows_tile) - a.g_shift;
-    int64_t units = 0, steps = 0, segs = 0;
+    int64_t units = 0, steps = 0;
     for (int x = 0; x < 2; ++x) {
         if (!l.with[x]) continue;
         const PagedLevel &lv = a.level[x];
@@ -493,7 +494,6 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
         const int64_t each = (lv.max_length + (1 << l.tile_shift) - 1) >> l.tile_shift;
         units += tiles * hkv;
         steps += tiles * hkv * each;
-        segs += lv.rows;
         // What paged_share goes by: prefixes are taken to be of the bound's length, own tokens of half.
         const int64_t each_row = (a.q_tokens + lv.rows - 1) / lv.rows;
         const double likely = (double)hkv * lv.rows * ((each_row + (1 << l.tt_shift) - 1) >> l.tt_shift);
@@ -504,8 +504,15 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     }
     l.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(steps, ctas_max));
     // (a run's end is its start plus a run's length, which the last run may pass by a step a CTA)
-    if (steps >= (1LL << 31) - 2 * PAGED_Q4_CTAS || units + l.ctas >= (1LL << 31)) return false;
-    l.slots = (int)(units + l.ctas);
+    if (steps >= (1LL << 31) - 2 * std::max(PAGED_MAX_CTAS, ctas_max) || units + l.ctas >= (1LL << 31)) return false;
+    l.slots = (int)units;  // (and one a CTA)
+    return true;
+}
+// Takes its buffers from the workspace at `off`.
+void paged_take(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, unsigned char *ws, size_t &off) {
+    const int rows_tile = 1 << (l.tt_shift + a.g_shift);
+    const int64_t segs = (l.with[0] ? a.level[0].rows : 0) + (l.with[1] ? a.level[1].rows : 0);
+    l.slots += l.ctas;
     auto take = [&](size_t bytes) {
         unsigned char *p = ws + off;
         off = align256(off + bytes);
@@ -514,6 +521,11 @@ bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows
     l.rec = (int2 *)take((size_t)(1 + segs) * 8);
     l.part_ml = (float *)take((size_t)l.slots * rows_tile * 2 * 4);
     l.part_o = (float *)take((size_t)l.slots * rows_tile * ctx->sh.head_dim * 4);
+}
+bool paged_line(const verkv_ctx *ctx, const PagedArgs &a, PagedLine &l, int rows_tile, int ctas_max, unsigned char *ws,
+                size_t &off) {
+    if (!paged_count(a, l, rows_tile, ctas_max)) return false;
+    paged_take(ctx, a, l, ws, off);
     return true;
 }
 
@@ -544,14 +556,18 @@ bool paged_share(PagedLine &wide, PagedLine &own, int sms) {
 // 8 sequences of up to 512 tokens behind 32K 87 us.)  A step is 1.7 us of a CTA, three of which fit on an SM of either
 // kind, or with 32 rows 1.9 of one of two, and a unit, which begins and ends alone, 8.  (With 3, 5, 8, 12 a unit: 32
 // sequences of up to 16 tokens behind 32K 138, 120, 116, 108 us, 8 behind 2048 21.1, 20.3, 20.7, 25.3.)  Where own
-// tokens are most of the work, all SMs take both.
-void paged_q4_share(PagedLine &prefix, PagedLine &own, int sms) {
+// tokens are most of the work, all SMs take both; of a call of 9 to 16 rows the prefix's tiles of 16 are one an SM then, for
+// which the workspace has room.
+void paged_q4_share(PagedLine &prefix, PagedLine &own, int sms, int64_t rows) {
     for (PagedLine *l : {&prefix, &own}) {
         l->per_sm = std::min(l->per_sm, 3);
         l->cost = (l->steps * (l->per_sm == 2 ? 1.9 : 1.7) + l->units * 8.0) / l->per_sm;
     }
     const int x = (int)(sms * own.cost / (own.cost + prefix.cost)) + 1;
-    if (x > sms * 3 / 4) return;
+    if (x > sms * 3 / 4) {
+        if (rows > 8 && rows <= 16) prefix.ctas = std::min(prefix.ctas, PAGED_MAX_CTAS * PAGED_ROWS / 16 - PAGED_Q4_CTAS_16);
+        return;
+    }
     own.ctas = std::min(own.ctas, own.per_sm * x);
     prefix.ctas = std::min(prefix.ctas, prefix.per_sm * (sms - x));
 }
@@ -1432,12 +1448,14 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
             const int tile = rows <= 8 ? 8 : rows <= 16 || sh.head_dim == 64 ? 16 : 32;
             l.per_sm = tile == 8 ? 4 : tile == 16 ? 3 : 2;
             const int most = tile == 8 ? PAGED_Q4_CTAS : tile == 16 ? PAGED_Q4_CTAS_16 : PAGED_Q4_CTAS_32;
-            if (!paged_line(ctx, a, l, tile, std::min(ctx->sms * l.per_sm, most), (unsigned char *)workspace, off))
+            if (!paged_count(a, l, tile, std::min(ctx->sms * l.per_sm, most)))
                 return fail(ctx, VERKV_EINVAL, "paged_attend: more than 2^31 steps of work in one call");
         }
-        if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
         const bool both_levels = lines[0].ctas && lines[1].ctas;
-        if (both_levels) paged_q4_share(lines[0], lines[1], ctx->sms);
+        if (both_levels) paged_q4_share(lines[0], lines[1], ctx->sms, (int64_t)q_tokens * sh.q_per_kv);
+        for (int x = 0; x < 2; ++x)
+            if (lines[x].ctas) paged_take(ctx, a, lines[x], (unsigned char *)workspace, off);
+        if (off > workspace_bytes) return fail(ctx, VERKV_EINVAL, "paged_attend: workspace too small");
         // (launches that are timed one by one wait for one another)
         if (both_levels && !ctx->prof_on) a.ready = (unsigned long long *)workspace;
         const int first = both_levels && lines[1].cost > lines[0].cost ? 1 : 0;  // the longer one
