@@ -465,8 +465,9 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
  * out goes along (2^-22, and of codes 2^-20).  Of weights far below a row's largest a token loses up to 2^-32 of
  * that, of its floors, and 15 2^-30 of it, of the largest step of its group of channels (of 2^-16 where
  * all of a group's steps are smaller); and where steps of 1 and more come, smaller ones are off by 2^-24 of them.  Units
- * have at most 16 rows there, so many queries of one sequence or prefix read its codes again for every 16
- * (from 128 rows on, 16-bit pages are the faster ones).  Over 16-bit pages the weights are multiplied
+ * have at most 16 rows (queries x q_per_kv) there, or 32 at head_dim 128, so many queries of one sequence or
+ * prefix read its codes again for each: up to 16 rows 4-bit pages are the faster ones, from about 32 rows on 16-bit
+ * ones.  Over 16-bit pages the weights are multiplied
  * with V as two parts of the pages' type, which hold them to 2^-16 (bf16) or 2^-22 (fp16); where
  * prefixes or sequences have more than 128 rows (queries x q_per_kv) on average, they are rounded to
  * the pages' type instead, and not in the sum they are divided by.

@@ -18,7 +18,7 @@
 // its latency: some 12 barriers, dependent loads (a length; weights; a list, a table, a row; a table, a row) and,
 // since most of it runs once, the fetch of its instructions, hence loops that are not unrolled.  Measured: 32
 // sequences x 8 heads of 2304 tokens down to 2048 (24 MB of rows read, 24 written) 17.1 us, of which choosing takes 5 and
-// the lists 2; four prompts of 8192 tokens down to 1024 16.0; 64 sequences of 4096 down to 1024 (426 MB) 84, 5.1 TB/s.
+// the lists 2; four prompts of 8192 tokens down to 1024 16.0; 64 sequences of 4096 down to 1024 (426 MB) 85, 5.0 TB/s.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -27,11 +27,13 @@
 // large ones: a token loses 2^-33 of the row's largest weight times its group's largest step.  (With steps as
 // they are, codes of values of 0.01 behind a token of 2^20 times the others' weight were off by a quarter.)
 //
-// Bound: with few rows the bytes, and the start, end and merge of a CTA's run (11-17 us): 32 sequences of up to
-// 16384 tokens (346 MB) 80 us, 0.64 of a plain copy's rate over all and 6.0 TB/s, 0.88, in the steady part (the same
-// ring without arithmetic 6.65).  With many rows the instructions that spread codes and scale products, which is why
-// units of 32 rows share them at d = 128: 32 rows behind 32K tokens 47 us, 128 rows 116.  Five CTAs an SM, rings of
-// three blocks and two blocks at a time gained nothing.
+// Bound: with few rows the bytes and, beside them, each CTA's start, end and changes of unit, where its ring stands
+// empty: 32 sequences of up to 16384 tokens (346 MB) 82 us, 0.62 of a plain copy's rate (over 16-bit pages 0.97).  With
+// many rows the dependences within a block -- codes to products to weights to products -- with the few warps that the
+// sums' registers leave: of 32 rows at d = 128 8 warps an SM issue in a quarter of the slots, and 32 rows behind 32K tokens take
+// 48 us, 128 rows 116.  Each unit spreads its codes again, so that from about 32 rows of a sequence or prefix on 16-bit
+// pages take less time.  Five CTAs an SM, rings of three blocks and two blocks at a time gained nothing, nor
+// did the groups' 2^k in shared memory.
 #include <math.h>
 
 #include <algorithm>

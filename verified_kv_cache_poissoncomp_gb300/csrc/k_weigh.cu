@@ -10,14 +10,18 @@
 // and a fixed order.  What lies behind a sequence's length is copied in pieces of 512 places a warp.
 //
 // k_weigh_few: up to about 8 rows a sequence (a decode step).  Bound by the keys' bytes (16 sequences of 16384 tokens, 550 MB:
-// 90 us, 6.1 TB/s, 0.90 of a plain copy's rate), over 4-bit pages by instructions (32 of up to 16384, 190 MB: 61 us, 0.46).  All sequences'
+// 90 us, 6.1 TB/s, 0.90 of a plain copy's rate), over 4-bit pages by its copies and its chains of products alike, with 16 warps an SM and 48 % of the issue slots (32
+// of up to 16384, 190 MB: 61 us, 0.46).  All sequences'
 // blocks of 16 tokens, end to end, are cut into equal runs, one a warp, which has a ring of blocks in shared
 // memory: its next two are on their way while it works on two (chains of products and exponentials side by side), or of 4-bit
 // pages seven while it works on one.  (One in place of two, 32 sequences of 2000-2048 tokens: 32.4 us, 27.1; two of 4-bit
 // pages, which leaves three CTAs of four an SM, 32 of up to 16384: 65.3 us, 61.5.)
 //
-// k_weigh_many: more rows (drafts; over 4-bit pages any number).  Bound by instructions (32 rows, four sequences of 8192
-// tokens: 28.5 us).  A CTA takes 128 tokens
+// k_weigh_many: more rows (drafts; over 4-bit pages any number).  16 rows, four sequences of 8192 tokens: 20.5 us, waiting
+// for an item's loads (lengths, table, keys), which are not on their way during the item before; over 4-bit pages 27.7,
+// and about 1 us for each row more (64 queries, 256 rows: 256 us for 28 over 16-bit pages), chains of mma.sync and
+// float32 sums with 12 warps an SM: 46 % of the issue slots, 15 % of the tensor pipe.  Nothing stands against a form of
+// k_weigh_wide over codes, which are exact there too; it has not been written.  A CTA takes 128 tokens
 // of one KV head, 32 a warp, whose keys stay in registers while 32 rows at a time pass through shared
 // memory, the next ones on their way meanwhile.
 //

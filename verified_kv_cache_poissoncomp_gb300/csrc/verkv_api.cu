@@ -1436,9 +1436,11 @@ verkv_status verkv_paged_attend(verkv_ctx *ctx, const verkv_pages *pages, int32_
     size_t off = 256;  // (the first word: PagedArgs::ready)
     if (packed(pages) && (a.level[0].rows || a.level[1].rows)) {
         // A launch of each level, side by side.  Units of 8 rows, or of 16 or 32 where segments have more: K and V's codes are
-        // then spread out less often.  (32 rows in place of 16, behind 32K tokens: 32 sequences 118 us for 134, 64 245
-        // for 275, 8 with up to 512 tokens of their own 47 for 53.  At d = 64 there is half as much to spread out, and two
-        // prefixes of 8191 with 17 sequences each take 61 us for 55.)
+        // then spread out less often, which long work gains by: 4 sequences of 8192 tokens by their last 64 queries
+        // take 164 us with units of 32 for 184 with 16, by 512 1176 for 1360, 8 sequences behind 131072 tokens 116 for 123.  Short
+        // work loses by longer units: 8 sequences behind 2048 tokens 21 for 18, 32 with 512 tokens of their own behind 32K
+        // 165 for 145, 8 there 47 for 49.  At d = 64 there is half as much to spread out: two prefixes of 8191 with
+        // 17 sequences each take 60 us with 32 for 54, 32 sequences behind 32K 61 for 69.
         for (int x = 0; x < 2; ++x) {
             PagedLine &l = lines[x];
             if (!a.level[x].rows) continue;

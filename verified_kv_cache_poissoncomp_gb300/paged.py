@@ -386,7 +386,8 @@ class PagedKV:
         and, between, those with the largest weights (float32 [sequences][kv_heads][places], as weigh adds
         them up).  Their rows move together in the sequence's pages, none of which may stand twice in the call's
         tables up to the lengths; afterwards every sequence has min(length, keep) tokens, and the caller sets the lengths once
-        every layer's call is made.  out: the weights in their tokens' new places, 0 behind them; by default
+        every layer's call is made.  From then on a token's place is not its position: append's index goes on from
+        the new lengths, its positions from the old ones.  out: the weights in their tokens' new places, 0 behind them; by default
         in weights' place.
 
         Returns (out, kept): kept int32 [sequences][kv_heads][keep] is the former place of the token that
