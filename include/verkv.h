@@ -464,7 +464,9 @@ verkv_status verkv_paged_append(verkv_ctx *ctx, const verkv_pages *pages, int32_
  * it meets codes (2^-10 in all), and not in the sum they are divided by; with binary16 rows what that leaves
  * out goes along (2^-22, and of codes 2^-20).  Of weights far below a row's largest a token loses up to 2^-32 of
  * that, of its floors, and 15 2^-30 of it, of the largest step of its group of channels (of 2^-16 where
- * all of a group's steps are smaller); and where steps of 1 and more come, smaller ones are off by 2^-24 of them.  Units
+ * all of a group's steps are smaller); and where steps of 1 and more come, smaller ones are off by 2^-24 of them.
+ * Sums over codes lose, an addend, up to 2^-15 (binary16 rows: 2^-19) of the largest weight among 16 tokens times the
+ * step; those of logits 2^-15 of the query's largest channel times the key's step, in each group.  Units
  * have at most 16 rows (queries x q_per_kv) there, or 32 at head_dim 128, so many queries of one sequence or
  * prefix read its codes again for each: up to 16 rows 4-bit pages are the faster ones, from about 32 rows on 16-bit
  * ones.  Over 16-bit pages the weights are multiplied

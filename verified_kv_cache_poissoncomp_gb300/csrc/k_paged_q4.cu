@@ -14,7 +14,7 @@
 //         bfloat16 results that is all: a weight is off by up to 2^-11, and 2^-11 more where it meets codes, little
 //         beside the result's own 2^-8 (1.66e-3 of o's root mean square, 1.65e-3 without).  Binary16 results
 //         would show it (5.5e-4 for 2.1e-4): there what either rounding leaves out goes along in an operand of
-//         its own (REST).  The sum that they are divided by is of the float32 weights
+//         its own (REST), and all codes are 16 n (q4.cuh; with n, a token of nearly all weight was off by 2^-12 of a step).  The sum that they are divided by is of the float32 weights
 //     O += V^T P     channels x rows, exact codes
 //     B += F^T P     groups x rows: the floors' part, the same for all channels of a group
 //
@@ -411,14 +411,14 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 #pragma unroll
                         for (int w = 0; w < VW; ++w) {
                             const uint32_t z = byte_pair(word_of(v[i][0], w), word_of(v[i][1], w), byte0 + x * NEXT_BYTE);
-                            va[0][2 * i + (w & 1)] = z & LOW4;
+                            va[0][2 * i + (w & 1)] = REST ? z << 4 & HIGH4 : z & LOW4;
                             va[1][2 * i + (w & 1)] = z & HIGH4;
                         }
                     } else {
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             const uint32_t z = byte_pair(word_of(v[i][0], 0), word_of(v[i][1], 0), byte0 + (2 * x + m) * NEXT_BYTE);
-                            va[m][2 * i] = z & LOW4;
+                            va[m][2 * i] = REST ? z << 4 & HIGH4 : z & LOW4;
                             va[m][2 * i + 1] = z & HIGH4;
                         }
                     }
@@ -490,9 +490,10 @@ __global__ void __launch_bounds__(PQ_NT, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                 const float f = exp2_fast(ref[n][e] - ms);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
-                    // channels 16 x + 2 g and the next one, or of d = 64 16 x + g and 8 more; codes of upper bits are 16 n
+                    // channels 16 x + 2 g and the next one, or of d = 64 16 x + g and 8 more; codes of upper bits are 16 n, with
+                    // REST all
                     float *at = buf + (warp * R + r) * D + 16 * x;
-                    const float lu = D == 128 && (x & 1) ? CODE_UNIT / 16 : CODE_UNIT, hu = D == 64 || (x & 1) ? CODE_UNIT / 16 : CODE_UNIT;
+                    const float lu = REST || (D == 128 && (x & 1)) ? CODE_UNIT / 16 : CODE_UNIT, hu = REST || D == 64 || (x & 1) ? CODE_UNIT / 16 : CODE_UNIT;
                     const float lo = fmaf(o[n][x][e], lu * back[x / 2], base[n][e][x / 2]) * f, hi = fmaf(o[n][x][e + 2], hu * back[x / 2], base[n][e][x / 2]) * f;
                     if (D == 128) {
                         *reinterpret_cast<float2 *>(at + 2 * g) = make_float2(lo, hi);
