@@ -14,7 +14,8 @@
 //         bfloat16 results that is all: a weight is off by up to 2^-11, and 2^-11 more where it meets codes, little
 //         beside the result's own 2^-8 (1.66e-3 of o's root mean square, 1.65e-3 without).  Binary16 results
 //         would show it (5.5e-4 for 2.1e-4): there what either rounding leaves out goes along in an operand of
-//         its own (REST), and all codes are 16 n (q4.cuh; with n, a token of nearly all weight was off by 2^-12 of a step).  The sum that they are divided by is of the float32 weights
+//         its own (REST), and all codes are 16 n (q4.cuh; with n, results near 0 were off by 1.4e-5 for 2e-6 of
+//         values of 1).  The sum that they are divided by is of the float32 weights
 //     O += V^T P     channels x rows, exact codes
 //     B += F^T P     groups x rows: the floors' part, the same for all channels of a group
 //
@@ -23,15 +24,15 @@
 // 2^14, the largest one so far 2^8 at least, and the last bit of a binary16 2^-24.  Steps meet it as step 2^k, with a k for each
 // group of V's channels that makes the largest one so far 1/2 to 2 (k <= 15, all that one product makes of binary16:
 // a group whose steps are all below 2^-16 stays below 1/2).  Where larger steps come k is lowered, with O scaled, by
-// the same vote.  So products are below 2^15, and as many bits of them remain in small values as in
-// large ones: a token loses 2^-33 of the row's largest weight times its group's largest step.  (With steps as
-// they are, codes of values of 0.01 behind a token of 2^20 times the others' weight were off by a quarter.)
+// the same vote.  So products are below 2^15, and as many bits of them remain in small values as in large ones: a
+// rounding of one loses 2^-32 at most of the row's largest weight times its group's largest step, for each of up to 15
+// of a code.  (With steps as they are, codes of values of 0.01 behind a token of 2^20 times the others' weight were lost.)
 //
 // Bound: with few rows the bytes and, beside them, each CTA's start, end and changes of unit, where its ring stands
 // empty: 32 sequences of up to 16384 tokens (346 MB) 82 us, 0.62 of a plain copy's rate (over 16-bit pages 0.97).  With
-// many rows the dependences within a block -- codes to products to weights to products -- with the few warps that the
-// sums' registers leave: of 32 rows at d = 128 8 warps an SM issue in a quarter of the slots, and 32 rows behind 32K tokens take
-// 48 us, 128 rows 116.  Each unit spreads its codes again, so that from about 32 rows of a sequence or prefix on 16-bit
+// many rows the dependences within a block -- codes to products to weights to products -- with the few warps that
+// the sums' registers leave: of 32 rows at d = 128 8 warps an SM issue in a quarter of the slots, and 32 rows behind 32K
+// tokens take 48 us, 128 rows 116.  Each unit spreads its codes again, so that from about 32 rows of a sequence or prefix on 16-bit
 // pages take less time.  Five CTAs an SM, rings of three blocks and two blocks at a time gained nothing, nor
 // did the groups' 2^k in shared memory.
 #include <math.h>

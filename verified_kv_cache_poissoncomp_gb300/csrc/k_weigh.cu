@@ -10,8 +10,8 @@
 // and a fixed order.  What lies behind a sequence's length is copied in pieces of 512 places a warp.
 //
 // k_weigh_few: up to about 8 rows a sequence (a decode step).  Bound by the keys' bytes (16 sequences of 16384 tokens, 550 MB:
-// 90 us, 6.1 TB/s, 0.90 of a plain copy's rate), over 4-bit pages by its copies and its chains of products alike, with 16 warps an SM and 48 % of the issue slots (32
-// of up to 16384, 190 MB: 61 us, 0.46).  All sequences'
+// 90 us, 6.1 TB/s, 0.90 of a plain copy's rate), over 4-bit pages by its copies and its chains of products alike, with
+// 16 warps an SM and 48 % of the issue slots (32 of up to 16384, 190 MB: 61 us, 0.46).  All sequences'
 // blocks of 16 tokens, end to end, are cut into equal runs, one a warp, which has a ring of blocks in shared
 // memory: its next two are on their way while it works on two (chains of products and exponentials side by side), or of 4-bit
 // pages seven while it works on one.  (One in place of two, 32 sequences of 2000-2048 tokens: 32.4 us, 27.1; two of 4-bit
